@@ -395,6 +395,40 @@ LA_API la_status la_prefill_backward_varlen(const void *q, const void *k, const 
                                             cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Causal softmax attention over packed prompts, with grouped key/value heads:
+ * the softmax layers that stand between the Lightning layers of the hybrid
+ * model ("MiniMax-01技术报告解读", §2.3: one in eight layers, 64 query heads in
+ * groups of 8 per key/value head).  Per sequence, for query head h and its
+ * key/value head h / (H / Hkv), with t counted from the sequence's start:
+ *
+ *     lse_t = log sum_{s <= t} exp(scale q_t . k_s)          (natural logarithm)
+ *     o_t   = sum_{s <= t} exp(scale q_t . k_s - lse_t) v_s
+ *
+ *   q            device bf16 [total_tokens, H, d];  k, v: [total_tokens, Hkv, d],
+ *                H a multiple of Hkv.
+ *   cu_seqlens, nseq, max_seqlen   as for la_prefill_varlen.
+ *   scale        a positive finite factor of the scores (usually d^-0.5).
+ *   out          device bf16 [total_tokens, H, d].
+ *   lse          device fp32 [total_tokens, H], or NULL.  The backward pass
+ *                needs it; with it partial results over disjoint keys can be
+ *                joined.
+ *   workspace    la_softmax_prefill_varlen_workspace_size bytes, 256-byte
+ *                aligned, as for la_prefill.
+ * Scores, maxima, sums and outputs are accumulated in fp32; the weights are
+ * rounded to bf16 once for the product with v.  A row depends on its own
+ * sequence alone; a value that is not finite in row s of v may reach earlier
+ * rows of the same sequence that lie in the same 128 rows as s.
+ * ------------------------------------------------------------------------- */
+LA_API size_t la_softmax_prefill_varlen_workspace_size(int nseq, int total_tokens, int H, int Hkv,
+                                                       int d);
+
+LA_API la_status la_softmax_prefill_varlen(const void *q, const void *k, const void *v,
+                                           const int *cu_seqlens, int nseq, int total_tokens,
+                                           int max_seqlen, int H, int Hkv, int d, float scale,
+                                           void *out, float *lse, void *workspace,
+                                           size_t ws_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Status.
  * la_get_device_status synchronises `stream`, then returns and clears the
  * sticky device word of the current device (LA_ERR_TIMEOUT,

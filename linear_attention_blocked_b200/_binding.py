@@ -28,7 +28,8 @@ EXPORTED = ("la_prefill_workspace_size", "la_prefill", "la_prefill_varlen_worksp
             "la_kv_aggregate_workspace_size", "la_kv_aggregate", "la_state_prefix",
             "la_prefill_backward_workspace_size", "la_prefill_backward", "la_prefill_decay",
             "la_prefill_varlen_decay", "la_decode_step_decay", "la_prefill_from_host_buffer_size",
-            "la_prefill_from_host", "la_prefill_backward_varlen_workspace_size", "la_prefill_backward_varlen")
+            "la_prefill_from_host", "la_prefill_backward_varlen_workspace_size", "la_prefill_backward_varlen",
+            "la_softmax_prefill_varlen_workspace_size", "la_softmax_prefill_varlen")
 
 
 class LAError(RuntimeError):
@@ -106,6 +107,12 @@ def lib():
         L.la_prefill_backward_varlen.argtypes = [vp, vp, vp, vp, vp, c_int, c_int, c_int, c_int, c_int, vp, vp, vp,
                                                  vp, vp, c_int, vp, vp, sz, vp]
         L.la_prefill_backward_varlen.restype = c_int
+        f32 = ctypes.c_float
+        L.la_softmax_prefill_varlen_workspace_size.argtypes = [c_int] * 5
+        L.la_softmax_prefill_varlen_workspace_size.restype = sz
+        L.la_softmax_prefill_varlen.argtypes = [vp, vp, vp, vp, c_int, c_int, c_int, c_int, c_int, c_int, f32, vp, vp,
+                                                vp, sz, vp]
+        L.la_softmax_prefill_varlen.restype = c_int
         L.la_get_device_status.argtypes = [vp]
         L.la_get_device_status.restype = c_int
         L.la_status_string.argtypes = [c_int]

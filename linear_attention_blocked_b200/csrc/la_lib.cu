@@ -14,6 +14,7 @@
 #include "la_aggregate.cuh"
 #include "la_decode.cuh"
 #include "la_prefill.cuh"
+#include "la_softmax.cuh"
 
 namespace {
 
@@ -1026,3 +1027,5 @@ extern "C" la_status la_prefill_noalloc(const void *q, const void *k, const void
     ++g_launches;
     return LA_OK;
 }
+
+#include "la_softmax_api.cuh"

@@ -1,0 +1,659 @@
+// la_softmax.cuh -- causal softmax attention over whole prompts for sm_100a,
+// with grouped key/value heads, on packed sequences or behind a paged cache.
+//
+// Per sequence and query head, with past cached tokens in front of its n new
+// ones and pos(t) = past + t:
+//
+//     o_t = sum_{s <= pos(t)} p_ts v_s,   p_ts = exp(scale q_t . k_s - lse_t)
+//     lse_t = log sum_{s <= pos(t)} exp(scale q_t . k_s)
+//
+// in one pass over the keys with a running maximum m and sum l per row:
+//     x = Q K_j^T,  m' = max(m, rowmax x),  P = 2^(c x - c m'),  c = scale log2 e
+//     l <- 2^(c m - c m') l + rowsum P,  O <- 2^(c m - c m') O + P V_j.
+// m may lag behind the true maximum as long as 2^(c x - c m) stays small: a row
+// rescales O only when its maximum has grown by more than 2^RESCALE_LOG2 since
+// the m in use (P then stays below 2^8, exact in fp32 sums; bf16 P has the same
+// relative rounding at any magnitude), which after the first tiles is rare.
+//
+// One CTA works on a pair of query tiles (128 rows of one query head each)
+// that read the same K and V tiles: two query heads of the same key/value
+// head and the same rows, or, where a group has an odd number of heads, the
+// pairs that its heads' tiles over 256 rows fall into.  Every step of a tile
+// is S = Q K_j^T (SS MMA), softmax by one warpgroup (a thread per row), and
+// O += P V_j (TS MMA, P as bf16 in TMEM over its scores).  The two tiles take
+// turns: the tensor pipe runs P V and the next S of one while the other is in
+// its softmax, so neither waits as long as a softmax is no slower than two
+// products (1024 cycles at 128 x 128 x 128).
+//
+// The tensor pipe runs MMAs in issue order, so S_{j+1} may be issued over the
+// buffer that P V_j reads, right behind it.
+//
+// Warp roles (512 threads, registers split by setmaxnreg):
+//   warp 0       items and K/V tiles (TMA)         warpgroup 0: 48 registers
+//   warp 1       TMEM allocator + MMA issuer
+//   warp 2       Q tiles (TMA)
+//   warps 4-7    softmax of tile 0                 192 registers
+//   warps 8-11   softmax of tile 1                 192 registers
+//   warps 12-15  output: O / l, lse                80 registers
+// Shared memory: Q 2 x 32 KiB | ring of 5 x 32 KiB K and V tiles in turn |
+// barriers.  TMEM (512 columns): S0 | S1 | O0 | O1.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include "la_prefill.cuh"
+#include "la_ptx.cuh"
+
+namespace la {
+
+constexpr int ST_CUDA = 3;  // device status code (matches la_status)
+
+constexpr int SMX_THREADS = 512;
+constexpr int SMX_STAGES = 5;
+constexpr int SMX_Q = 0;
+constexpr int SMX_KV = 2 * TILE_BYTES;
+constexpr int SMX_CTRL = SMX_KV + SMX_STAGES * TILE_BYTES;
+constexpr int SMX_STAT = SMX_CTRL + 512;                    // {c m, l} of both tiles' rows
+constexpr int SMX_SMEM = SMX_STAT + 2 * BLK * 8;            // (1024-byte aligned as it is)
+static_assert(SMX_SMEM <= 227 * 1024, "shared memory of one CTA");
+constexpr uint32_t SMX_TM_S = 0, SMX_TM_O = 256;            // tile t: + 128 t
+constexpr int HDR_TICKET2 = 3;                              // second ticket counter of the workspace header
+constexpr int SMX_SLOTS = 4;                                // item queue
+constexpr float RESCALE_LOG2 = 8.f;
+
+// Entries: the row blocks of every sequence, sequence by sequence, each from
+// its last block (the longest row of keys) to its first.
+struct SoftmaxScheduleParams {
+    const int *cu;            // device cu_seqlens [nseq + 1]
+    const int *past;          // device [nseq] cached tokens, or null (none)
+    int nseq, T, max_seqlen;
+    long long max_keys;       // bound on past + new tokens of a sequence (paged)
+    int rows;                 // rows per entry: 128 or 256
+    int items_per_entry;
+    int *hdr;                 // workspace header
+    int *prefix;              // [nseq + 1] entries before each sequence
+    int4 *entries;            // {sequence, first token, length, block}
+    int *status;
+};
+
+struct SoftmaxPrefillParams {
+    __nv_bfloat16 *out;       // [T, H, D]
+    float *lse;               // [T, H]
+    int *hdr;
+    const int4 *entries;
+    const int *past;          // device [nseq] or null
+    const int *pages;         // device [nseq, max_pages] page table, or null (packed K and V)
+    int max_pages, n_pages, page, page_shift;
+    int H, Hkv, G;
+    int pairs;                // pairs of query tiles per entry
+    int rows;
+    float scale_log2;         // scale * log2(e)
+    unsigned long long wait_limit_ns;
+    int *status;
+};
+
+// item fields
+enum { SI_VALID = 0, SI_H0, SI_H1, SI_B0, SI_B1, SI_N0, SI_N1, SI_TOK0, SI_LEN, SI_PAST, SI_KVH, SI_SEQ, SI_FIELDS };
+
+struct SoftmaxCtrl {
+    uint64_t kv_full[SMX_STAGES], kv_empty[SMX_STAGES];
+    uint64_t q_full[2], q_empty[2];   // per tile
+    uint64_t s_full[2];               // [1] scores of the tile's next step
+    uint64_t p_full[2];               // [4] P of the step in TMEM (and O rescaled)
+    uint64_t o_full[2];               // [1] all of an item's P V added to O
+    uint64_t o_empty[2];              // [4] output warps have read O
+    uint64_t stat_full[2];            // [4] m and l of the tile's rows written
+    uint64_t stat_empty[2];           // [4] output warps have read them
+    uint64_t item_full[SMX_SLOTS];    // [1]
+    uint64_t item_empty[SMX_SLOTS];   // [14] Q, MMA, 8 softmax and 4 output warps
+    uint64_t fin;                     // [1] tear-down: every MMA done
+    int item[SMX_SLOTS][12];
+    uint32_t tmem_base;
+    volatile int abort;
+};
+static_assert(sizeof(SoftmaxCtrl) <= 512, "control block");
+static_assert(SI_FIELDS <= 12, "item fields");
+
+template <int N>
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// 2^x (the PTX instruction: relative error 2^-22, 0 for -inf)
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Bounded waits of a control block with `abort`: as wait_or_abort above.
+template <class Ctrl>
+__device__ __forceinline__ bool ctrl_wait(uint64_t *bar, uint32_t parity, unsigned long long limit_ns, int *status,
+                                          Ctrl *cb) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (la_wait(bar, parity, globaltimer_ns() + limit_ns, &cb->abort)) return true;
+    cb->abort = 1;
+    record_status(status, ST_TIMEOUT);
+    return false;
+}
+template <class Ctrl>
+__device__ __forceinline__ bool ctrl_warp_wait(uint64_t *bar, uint32_t parity, unsigned long long limit_ns,
+                                               int *status, Ctrl *cb) {
+    return __all_sync(0xffffffffu, ctrl_wait(bar, parity, limit_ns, status, cb)) != 0;
+}
+
+// The next item of the queue; a role reads the fields of its MASK.
+template <uint32_t MASK>
+__device__ __forceinline__ bool smx_next(uint32_t &it, int (&item)[SI_FIELDS], int lane,
+                                         const SoftmaxPrefillParams &p, SoftmaxCtrl *cb) {
+    const int slot = it % SMX_SLOTS;
+    item[SI_VALID] = 0;
+    if (!ctrl_warp_wait(&cb->item_full[slot], (it / SMX_SLOTS) & 1, p.wait_limit_ns, p.status, cb)) return false;
+#pragma unroll
+    for (int f = 0; f < SI_FIELDS; ++f)
+        if (f == SI_VALID || ((MASK >> f) & 1)) item[f] = __shfl_sync(0xffffffffu, cb->item[slot][f], 0);
+    if (lane == 0) mbar_arrive(&cb->item_empty[slot]);
+    ++it;
+    return item[SI_VALID] != 0;
+}
+
+// The item of ticket t: key/value head (outermost, so that the CTAs at work
+// share its keys in L2), entry, pair of tiles.
+__device__ __forceinline__ void smx_item(int t, int ne, const SoftmaxPrefillParams &p, int *item) {
+    const int per_head = ne * p.pairs;
+    const int kvh = t / per_head;
+    const int rest = t - kvh * per_head;
+    const int e = rest / p.pairs, pair = rest - e * p.pairs;
+    const int4 en = p.entries[e];
+    const int past = p.past ? p.past[en.x] : 0;
+    const int bpe = p.rows / BLK;  // blocks per entry
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const int u = 2 * pair + w;
+        const int b = en.w * bpe + u / p.G;
+        const int row = b * BLK;
+        // keys that the tile's last row sees
+        const int keys = past + min(row + BLK, en.z);
+        item[SI_H0 + w] = kvh * p.G + u % p.G;
+        item[SI_B0 + w] = b;
+        item[SI_N0 + w] = (u < bpe * p.G && row < en.z) ? (keys + BLK - 1) / BLK : 0;
+    }
+    item[SI_TOK0] = en.y;
+    item[SI_LEN] = en.z;
+    item[SI_PAST] = past;
+    item[SI_KVH] = kvh;
+    item[SI_SEQ] = en.x;
+}
+
+// One K or V tile: rows [row, row + 128) of a packed tensor, or the pages that
+// hold keys [key0, key0 + 128) of a sequence with `keys` of them.  Called by a
+// whole warp; with pages, lane i brings page i of the tile (both halves), and
+// what lies behind the last key is not loaded.
+__device__ __forceinline__ void smx_load_tile(uint8_t *dst, const CUtensorMap *tm, uint64_t *bar, int kvh, int row,
+                                              int key0, int keys, int pid, int lane, uint64_t pol,
+                                              const SoftmaxPrefillParams &p) {
+    if (!p.pages) {
+        if (lane == 0) {
+            mbar_expect_tx(bar, TILE_BYTES);
+            tma_load_4d(dst, tm, bar, 0, kvh, row, 0, pol);
+        }
+        return;
+    }
+    const int left = min(keys - key0, BLK);
+    const int np = (left + p.page - 1) >> p.page_shift;
+    if (lane == 0) mbar_expect_tx(bar, (uint32_t)(np * p.page * D * 2));
+    __syncwarp();
+    if (lane < np) {
+        const int r = (int)(((long long)pid * p.Hkv + kvh) << p.page_shift);
+        uint8_t *at = dst + lane * p.page * 128;
+        tma_load_3d(at, tm, bar, 0, r, 0, pol);
+        tma_load_3d(at + HALF_BYTES, tm, bar, 0, r, 1, pol);
+    }
+}
+
+__global__ void __launch_bounds__(SMX_THREADS, 1)
+la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                          const __grid_constant__ CUtensorMap tmv, const __grid_constant__ SoftmaxPrefillParams p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    SoftmaxCtrl *cb = reinterpret_cast<SoftmaxCtrl *>(smem + SMX_CTRL);
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const uint32_t sbase = smem_u32(smem);
+    if (sbase & 1023) {  // the swizzle needs it; dynamic shared memory starts there when there is no static
+        if (threadIdx.x == 0) record_status(p.status, ST_CUDA);
+        return;
+    }
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < SMX_STAGES; ++s) {
+            mbar_init(&cb->kv_full[s], 1);
+            mbar_init(&cb->kv_empty[s], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&cb->q_full[t], 1);
+            mbar_init(&cb->q_empty[t], 1);
+            mbar_init(&cb->s_full[t], 1);
+            mbar_init(&cb->p_full[t], 4);
+            mbar_init(&cb->o_full[t], 1);
+            mbar_init(&cb->o_empty[t], 4);
+            mbar_init(&cb->stat_full[t], 4);
+            mbar_init(&cb->stat_empty[t], 4);
+        }
+        for (int s = 0; s < SMX_SLOTS; ++s) {
+            mbar_init(&cb->item_full[s], 1);
+            mbar_init(&cb->item_empty[s], 14);
+        }
+        mbar_init(&cb->fin, 1);
+        cb->abort = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&tmq);
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+    }
+    if (warp == 1) {
+        tmem_alloc(&cb->tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, cb->tmem_base, 0);
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        return ctrl_warp_wait(bar, parity, p.wait_limit_ns, p.status, cb);
+    };
+
+    if (warp < 4) {
+        reg_dec<48>();
+        if (warp == 0) {
+            // ===================== items, K and V tiles =====================
+            const uint64_t pol = policy_evict_last();
+            const int total = p.hdr[HDR_TOTAL], ne = p.hdr[HDR_G];
+            uint32_t it = 0, n = 0;
+            bool ok = true;
+            for (;;) {
+                const int slot = it % SMX_SLOTS;
+                if (!wait(&cb->item_empty[slot], ((it / SMX_SLOTS) & 1) ^ 1)) { ok = false; break; }
+                int t = 0;
+                if (lane == 0) {
+                    t = atomicAdd(&p.hdr[HDR_TICKET], 1);
+                    cb->item[slot][SI_VALID] = t < total;
+                    if (t < total) smx_item(t, ne, p, cb->item[slot]);
+                }
+                t = __shfl_sync(0xffffffffu, t, 0);
+                __syncwarp();
+                const int n0 = cb->item[slot][SI_N0], n1 = cb->item[slot][SI_N1];
+                const int kvh = cb->item[slot][SI_KVH], tok0 = cb->item[slot][SI_TOK0];
+                const int keys = cb->item[slot][SI_PAST] + cb->item[slot][SI_LEN];
+                const int seq = cb->item[slot][SI_SEQ];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&cb->item_full[slot]);
+                ++it;
+                if (t >= total) break;
+                const int nmax = max(n0, n1);
+                for (int j = 0; j < nmax && ok; ++j) {
+                    int pid = 0;
+                    if (p.pages) {
+                        const int i = (j << (7 - p.page_shift)) + lane;  // page of this lane in the tile
+                        if (lane < (BLK >> p.page_shift) && (i << p.page_shift) < keys) {
+                            pid = p.pages[(size_t)seq * p.max_pages + i];
+                            if (pid < 0 || pid >= p.n_pages) {  // nothing outside the pool is read
+                                record_status(p.status, ST_INVALID);
+                                pid = 0;
+                            }
+                        }
+                    }
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const int s = n % SMX_STAGES;
+                        if (!wait(&cb->kv_empty[s], ((n / SMX_STAGES) & 1) ^ 1)) { ok = false; break; }
+                        smx_load_tile(smem + SMX_KV + s * TILE_BYTES, kv ? &tmv : &tmk, &cb->kv_full[s], kvh,
+                                      tok0 + j * BLK, j * BLK, keys, pid, lane, pol, p);
+                        ++n;
+                    }
+                }
+                if (!ok) break;
+            }
+            // every issued copy must land before the CTA exits
+            const uint32_t first = n > SMX_STAGES ? n - SMX_STAGES : 0;
+            for (uint32_t i = first; i < n; ++i) {
+                int dummy = 0;
+                la_wait(&cb->kv_full[i % SMX_STAGES], (i / SMX_STAGES) & 1, globaltimer_ns() + p.wait_limit_ns, &dummy);
+            }
+            if (!ok) cb->abort = 1;
+        } else if (warp == 1) {
+            // ===================== MMA issuer =====================
+            constexpr uint32_t ID_QK = idesc_bf16_f32(BLK, BLK, 0, 0);  // Q (K-major) x K (K-major)
+            constexpr uint32_t ID_PV = idesc_bf16_f32(BLK, D, 0, 1);    // P (TMEM) x V (MN-major)
+            uint32_t it = 0;
+            int cur[SI_FIELDS], nxt[SI_FIELDS];
+            uint32_t base = 0;                 // ring position of the current item's first K tile
+            // bit t: phase of the tile's Q, P and O barriers
+            uint32_t qph = 0, pph = 0, oph = 0;
+            uint32_t pend = 3;                 // bit t: first scores of the tile's next item not issued yet
+            constexpr uint32_t MASK = 1u << SI_N0 | 1u << SI_N1 | 1u << SI_PAST | 1u << SI_LEN;
+            bool ok = smx_next<MASK>(it, cur, lane, p, cb);
+            // S_t of step j of an item whose first K tile is at ring position rb
+            auto scores = [&](int t, const int (&im)[SI_FIELDS], uint32_t rb, int j) -> bool {
+                const uint32_t pos = rb + 2 * j, s = pos % SMX_STAGES;
+                const int nt = t ? im[SI_N1] : im[SI_N0], n1 = im[SI_N1];
+                if (j == 0) {
+                    if (!wait(&cb->q_full[t], (qph >> t) & 1)) return false;
+                    qph ^= 1u << t;
+                }
+                if (!wait(&cb->kv_full[s], (pos / SMX_STAGES) & 1)) return false;
+                tc_fence_after();
+                const uint32_t qt = sbase + SMX_Q + t * TILE_BYTES, kt = sbase + SMX_KV + s * TILE_BYTES;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_ss_w(tmem + SMX_TM_S + t * 128, desc_kmajor(qt, kk), desc_kmajor(kt, kk), ID_QK, kk > 0 ? 1u : 0u);
+                tc_commit_w(&cb->s_full[t]);
+                if (t == 1 || j >= n1) tc_commit_w(&cb->kv_empty[s]);  // last reader of the K tile
+                if (j == nt - 1) tc_commit_w(&cb->q_empty[t]);
+                return true;
+            };
+            while (ok) {
+                const int n0 = cur[SI_N0], n1 = cur[SI_N1], nmax = max(n0, n1);
+                const int keys = cur[SI_PAST] + cur[SI_LEN];
+                bool have_nxt = false, nxt_valid = false;
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (((pend >> t) & 1) && (t ? n1 : n0) > 0) {
+                        ok = scores(t, cur, base, 0);
+                        pend &= ~(1u << t);
+                    }
+                }
+                for (int j = 0; j < nmax && ok; ++j) {
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        const int nt = t ? n1 : n0;
+                        if (j >= nt) continue;
+                        const uint32_t pos = base + 2 * j + 1, s = pos % SMX_STAGES;
+                        uint8_t *vp = smem + SMX_KV + s * TILE_BYTES;
+                        if (!wait(&cb->kv_full[s], (pos / SMX_STAGES) & 1)) { ok = false; break; }
+                        const int valid = keys - j * BLK;
+                        if (valid < BLK && (t == 0 || j >= n0)) {
+                            // rows behind the last key meet P = 0, which keeps out what they
+                            // hold only if it is finite: zero them
+                            const int nbytes = (BLK - valid) * 128;
+                            for (int hh = 0; hh < 2; ++hh)
+                                for (int o = lane * 16; o < nbytes; o += 32 * 16)
+                                    *reinterpret_cast<uint4 *>(vp + hh * HALF_BYTES + valid * 128 + o) = make_uint4(0, 0, 0, 0);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                        if (j == 0) {
+                            if (!wait(&cb->o_empty[t], ((oph >> t) & 1) ^ 1)) { ok = false; break; }
+                            oph ^= 1u << t;
+                        }
+                        if (!wait(&cb->p_full[t], (pph >> t) & 1)) { ok = false; break; }
+                        pph ^= 1u << t;
+                        tc_fence_after();
+                        const uint32_t vt = smem_u32(vp);
+#pragma unroll
+                        for (int kk = 0; kk < BLK / 16; ++kk)
+                            mma_ts_w(tmem + SMX_TM_O + t * 128, tmem + SMX_TM_S + t * 128 + kk * 8, desc_mnmajor(vt, kk),
+                                     ID_PV, (j > 0 || kk > 0) ? 1u : 0u);
+                        if (t == 1 || j >= n1) tc_commit_w(&cb->kv_empty[s]);  // last reader of the V tile
+                        if (j + 1 < nt) {
+                            ok = scores(t, cur, base, j + 1);
+                        } else {
+                            tc_commit_w(&cb->o_full[t]);
+                            if (!have_nxt) {
+                                have_nxt = true;
+                                nxt_valid = smx_next<MASK>(it, nxt, lane, p, cb);
+                                if (cb->abort) ok = false;
+                            }
+                            pend |= 1u << t;
+                            if (ok && nxt_valid && (t ? nxt[SI_N1] : nxt[SI_N0]) > 0) {
+                                ok = scores(t, nxt, base + 2 * nmax, 0);
+                                pend &= ~(1u << t);
+                            }
+                        }
+                    }
+                }
+                if (!ok) break;
+                if (!have_nxt) nxt_valid = smx_next<MASK>(it, nxt, lane, p, cb);
+                base += 2 * nmax;
+                if (!nxt_valid) break;
+#pragma unroll
+                for (int f = 0; f < SI_FIELDS; ++f)
+                    if ((MASK >> f) & 1) cur[f] = nxt[f];
+            }
+            tc_commit_w(&cb->fin);
+            int dummy = 0;
+            la_wait(&cb->fin, 0, globaltimer_ns() + p.wait_limit_ns, &dummy);
+        } else if (warp == 2) {
+            // ===================== Q tiles =====================
+            const uint64_t pol = policy_evict_first();
+            constexpr uint32_t MASK = ~(1u << SI_PAST | 1u << SI_KVH | 1u << SI_SEQ | 1u << SI_LEN);
+            uint32_t it = 0, n[2] = {0, 0};
+            int im[SI_FIELDS];
+            bool ok = true;
+            while (ok && smx_next<MASK>(it, im, lane, p, cb)) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if ((t ? im[SI_N1] : im[SI_N0]) == 0) continue;
+                    if (!wait(&cb->q_empty[t], (n[t] & 1) ^ 1)) { ok = false; break; }
+                    if (lane == 0) {
+                        mbar_expect_tx(&cb->q_full[t], TILE_BYTES);
+                        tma_load_4d(smem + SMX_Q + t * TILE_BYTES, &tmq, &cb->q_full[t], 0, t ? im[SI_H1] : im[SI_H0],
+                                    im[SI_TOK0] + (t ? im[SI_B1] : im[SI_B0]) * BLK, 0, pol);
+                    }
+                    ++n[t];
+                }
+            }
+            for (int t = 0; t < 2; ++t)
+                if (n[t] > 0) {
+                    int dummy = 0;
+                    la_wait(&cb->q_full[t], (n[t] - 1) & 1, globaltimer_ns() + p.wait_limit_ns, &dummy);
+                }
+        }
+    } else if (warp < 12) {
+        // ===================== softmax of tile t =====================
+        reg_inc<192>();
+        const int t = (warp - 4) >> 2;
+        const int r = (warp & 3) * 32 + lane;
+        const uint32_t trow = tmem + ((uint32_t)(warp & 3) << 21);  // lanes of this warp's quarter
+        const uint32_t ts = trow + SMX_TM_S + t * 128, to = trow + SMX_TM_O + t * 128;
+        float2 *stat = reinterpret_cast<float2 *>(smem + SMX_STAT) + t * BLK;
+        const float c = p.scale_log2;
+        uint32_t it = 0, sn = 0, in = 0;
+        int im[SI_FIELDS];
+        bool ok = true;
+        constexpr uint32_t MASK = 1u << SI_N0 | 1u << SI_N1 | 1u << SI_B0 | 1u << SI_B1 | 1u << SI_PAST;
+        while (ok && smx_next<MASK>(it, im, lane, p, cb)) {
+            const int nt = t ? im[SI_N1] : im[SI_N0];
+            if (nt == 0) continue;
+            const int row = (t ? im[SI_B1] : im[SI_B0]) * BLK;
+            const int pos = im[SI_PAST] + row + r;  // the row's own position among the keys
+            const int first = im[SI_PAST] + row;    // that of the tile's first row
+            float m = -INFINITY, l = 0.f;           // m: maximum in use
+            for (int j = 0; j < nt; ++j) {
+                if (!wait(&cb->s_full[t], sn & 1)) { ok = false; break; }
+                tc_fence_after();
+                uint32_t x[128];
+                tmem_ld_cols<128>(ts, x);
+                if (j * BLK + BLK - 1 > first) {
+                    const int lim = pos - j * BLK;  // columns [0, lim] are seen
+#pragma unroll
+                    for (int i = 0; i < 128; ++i)
+                        if (i > lim) x[i] = 0xff800000u;  // -inf
+                }
+                float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < 128; ++i) mt[i & 3] = fmaxf(mt[i & 3], __uint_as_float(x[i]));
+                const float tile_max = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+                if (j == 0) {
+                    m = tile_max;
+                } else {
+                    const bool grow = (tile_max - m) * c > RESCALE_LOG2;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float alpha = grow ? ex2((m - tile_max) * c) : 1.f;
+                        if (grow) m = tile_max;
+                        l *= alpha;
+                        // O is complete up to the previous step: these scores were
+                        // issued, and so committed, behind its P V
+#pragma unroll 1
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t o[32];
+                            tmem_ld_wait32(to + q * 32, o);
+                            scale32(o, alpha);
+                            tmem_st32(to + q * 32, o);
+                        }
+                    }
+                }
+                const float mc = m * c;
+                float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {  // 32 columns at a time: 16 TMEM columns of bf16 pairs
+                    uint32_t b[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float e0 = ex2(fmaf(__uint_as_float(x[q * 32 + 2 * i]), c, -mc));
+                        const float e1 = ex2(fmaf(__uint_as_float(x[q * 32 + 2 * i + 1]), c, -mc));
+                        s4[(2 * i) & 3] += e0;
+                        s4[(2 * i + 1) & 3] += e1;
+                        b[i] = pack_bf16x2(e0, e1);  // one rounding to bf16, for the tensor cores
+                    }
+                    tmem_st16(ts + q * 16, b);
+                }
+                l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&cb->p_full[t]);
+                ++sn;
+            }
+            if (!ok) break;
+            if (!wait(&cb->stat_empty[t], (in & 1) ^ 1)) break;
+            stat[r] = make_float2(m * c, l);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&cb->stat_full[t]);
+            ++in;
+        }
+    } else {
+        // ===================== output =====================
+        reg_dec<80>();
+        const int r = (warp & 3) * 32 + lane;
+        const uint32_t trow = tmem + ((uint32_t)(warp & 3) << 21);
+        uint32_t it = 0, n[2] = {0, 0};
+        int im[SI_FIELDS];
+        bool ok = true;
+        constexpr uint32_t MASK = ~(1u << SI_PAST | 1u << SI_KVH | 1u << SI_SEQ);
+        while (ok && smx_next<MASK>(it, im, lane, p, cb)) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if ((t ? im[SI_N1] : im[SI_N0]) == 0) continue;
+                const float2 *stat = reinterpret_cast<const float2 *>(smem + SMX_STAT) + t * BLK;
+                if (!wait(&cb->stat_full[t], n[t] & 1)) { ok = false; break; }
+                const float2 ml = stat[r];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&cb->stat_empty[t]);
+                if (!wait(&cb->o_full[t], n[t] & 1)) { ok = false; break; }
+                ++n[t];
+                tc_fence_after();
+                const int row = (t ? im[SI_B1] : im[SI_B0]) * BLK + r, h = t ? im[SI_H1] : im[SI_H0];
+                const bool mine = row < im[SI_LEN];  // rows behind the sequence are left as they are
+                const size_t at = ((size_t)im[SI_TOK0] + row) * p.H + h;
+                const float inv = 1.f / ml.y;
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t o[32];
+                    tmem_ld_wait32(trow + SMX_TM_O + t * 128 + q * 32, o);
+                    if (mine) {
+                        uint4 *to = reinterpret_cast<uint4 *>(p.out + at * D + q * 32);
+                        scale32(o, inv);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]), __uint_as_float(o[8 * i + 2 * k + 1]));
+                            to[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&cb->o_empty[t]);
+                if (mine && p.lse) p.lse[at] = (ml.x + log2f(ml.y)) * 0.69314718055994531f;  // ln 2
+            }
+        }
+    }
+
+    // ===================== tear-down =====================
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Scheduler of the softmax kernels: checks cu_seqlens and the cached lengths,
+// writes the entries and resets the tickets.  One block.
+__global__ void __launch_bounds__(SCHED_THREADS, 1) la_softmax_schedule_kernel(const SoftmaxScheduleParams s) {
+    __shared__ int warp_sums[SCHED_THREADS / 32];
+    __shared__ int carry_sh;
+    const int tid = threadIdx.x;
+    int bad = 0;
+    if (tid == 0 && (s.cu[0] != 0 || s.cu[s.nseq] != s.T)) bad = 1;
+    for (int i = tid; i < s.nseq; i += SCHED_THREADS) {
+        const int a = s.cu[i], b = s.cu[i + 1];
+        if (a < 0 || b < a || b > s.T || b - a > s.max_seqlen) bad = 1;
+        if (s.past && b > a) {
+            const int past = s.past[i];
+            if (past < 0 || (long long)past + (b - a) > s.max_keys) bad = 1;
+        }
+    }
+    bad = __syncthreads_or(bad);
+    if (tid == 0) {
+        s.hdr[HDR_TICKET] = 0;
+        s.hdr[HDR_TICKET2] = 0;
+        carry_sh = 0;
+        if (bad) {
+            s.hdr[HDR_TOTAL] = 0;
+            s.hdr[HDR_G] = 0;
+            atomicCAS(s.status, 0, ST_INVALID);
+        }
+    }
+    if (bad) return;
+    __syncthreads();
+    for (int base = 0; base < s.nseq; base += SCHED_THREADS) {  // exclusive scan of entry counts
+        const int i = base + tid;
+        const int n = i < s.nseq ? (s.cu[i + 1] - s.cu[i] + s.rows - 1) / s.rows : 0;
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if ((tid & 31) >= o) x += y;
+        }
+        if ((tid & 31) == 31) warp_sums[tid >> 5] = x;
+        __syncthreads();
+        if (tid < 32) {
+            int w = warp_sums[tid];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, w, o);
+                if (tid >= o) w += y;
+            }
+            warp_sums[tid] = w;
+        }
+        __syncthreads();
+        if (i < s.nseq) s.prefix[i] = carry_sh + x - n + ((tid >> 5) ? warp_sums[(tid >> 5) - 1] : 0);
+        __syncthreads();
+        if (tid == 0) carry_sh += warp_sums[SCHED_THREADS / 32 - 1];
+        __syncthreads();
+    }
+    const int ne = carry_sh;
+    for (int e = tid; e < ne; e += SCHED_THREADS) {
+        int lo = 0, hi = s.nseq - 1;  // the last sequence whose first entry is at or before e
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s.prefix[mid] <= e) lo = mid;
+            else hi = mid - 1;
+        }
+        const int a = s.cu[lo], len = s.cu[lo + 1] - a;
+        const int nb = (len + s.rows - 1) / s.rows;
+        s.entries[e] = make_int4(lo, a, len, nb - 1 - (e - s.prefix[lo]));
+    }
+    if (tid == 0) {
+        s.hdr[HDR_G] = ne;
+        s.hdr[HDR_TOTAL] = ne * s.items_per_entry;
+    }
+}
+
+}  // namespace la

@@ -1,0 +1,96 @@
+"""Softmax attention for the layers that stand between the Lightning layers of
+the hybrid model: argument marshalling over the C ABI, as in `_binding`.
+
+A call runs on the device of `q` and on `stream` (default: that device's
+current stream); what it allocates -- outputs that were not passed, and the
+workspace -- belongs to that stream.
+"""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+from ._binding import D, _check, _need, _ptr, _stream_handle, lib
+
+SCALE = D ** -0.5
+
+
+@contextlib.contextmanager
+def _on(q, stream):
+    """Run on q's device and `stream`; yields the stream's handle."""
+    with torch.cuda.device(q.device):
+        if stream is None:
+            yield _stream_handle(torch.cuda.current_stream(q.device))
+            return
+        if stream.device != q.device:
+            raise ValueError("stream must be on the device of q")
+        with torch.cuda.stream(stream):
+            yield _stream_handle(stream)
+
+
+def _same_device(q, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != q.device:
+            raise ValueError(f"{name} must be on the device of q")
+
+
+def _need_qkv(q, k, v):
+    """Shapes of packed q [T, H, d], k and v [T, Hkv, d]: (T, H, Hkv, d)."""
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{name} must be [T, heads, d]")
+    T, H, d = q.shape
+    Hkv = k.shape[1]
+    _need(q, "q", torch.bfloat16, (T, H, d))
+    _need(k, "k", torch.bfloat16, (T, Hkv, d))
+    _need(v, "v", torch.bfloat16, (T, Hkv, d))
+    if Hkv == 0 or H == 0 or H % Hkv:
+        raise ValueError("the heads of q must be a multiple of those of k and v")
+    return T, H, Hkv, d
+
+
+def _scale(scale):
+    return SCALE if scale is None else float(scale)
+
+
+def _workspace(workspace, nbytes, device):
+    if workspace is None:
+        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace
+
+
+def _outputs(q, out, lse, want_lse, out_dtype=torch.bfloat16):
+    T, H, d = q.shape
+    if out is None:
+        out = torch.empty((T, H, d), dtype=out_dtype, device=q.device)
+    _need(out, "out", out.dtype if out_dtype is None else out_dtype, (T, H, d))
+    if lse is None and want_lse:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (T, H))
+    return out, lse
+
+
+def softmax_prefill_varlen(q, k, v, cu_seqlens, max_seqlen: int, scale=None, out=None, lse=None,
+                           want_lse: bool = True, workspace=None, stream=None):
+    """la_softmax_prefill_varlen: causal softmax attention of packed bf16
+    q [T, H, d] over k, v [T, Hkv, d] (H a multiple of Hkv) with device int32
+    cu_seqlens.  scale: factor of the scores, d**-0.5 by default.  Returns
+    (out [T, H, d] bf16, lse [T, H] fp32 or None)."""
+    T, H, Hkv, d = _need_qkv(q, k, v)
+    _need(cu_seqlens, "cu_seqlens", torch.int32)
+    nseq = cu_seqlens.numel() - 1
+    if nseq < 0:
+        raise ValueError("cu_seqlens must hold nseq + 1 entries")
+    _same_device(q, k=k, v=v, cu_seqlens=cu_seqlens, out=out, lse=lse, workspace=workspace)
+    with _on(q, stream) as handle:
+        out, lse = _outputs(q, out, lse, want_lse)
+        workspace = _workspace(workspace, lib().la_softmax_prefill_varlen_workspace_size(nseq, T, H, Hkv, d), q.device)
+        st = lib().la_softmax_prefill_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), nseq, T, int(max_seqlen), H,
+                                             Hkv, d, _scale(scale), _ptr(out), _ptr(lse), _ptr(workspace),
+                                             workspace.numel() * workspace.element_size(), handle)
+    _check(st, "la_softmax_prefill_varlen")
+    return out, lse

@@ -1,0 +1,70 @@
+"""Plain 64-bit softmax attention for the GPU tests, and the bounds that the
+kernels' roundings allow.
+
+Half a step of bf16 is eps/2 = 2^-8 of a value.  The prefill kernel rounds the
+weights once to bf16 and the output once to bf16, everything else is fp32, so
+
+    |out - exact| <= 2^-8 |exact| + 2^-8 A + f,   A = sum_s p_ts |v_s|
+
+(the second term: each p_ts is off by at most 2^-8 p_ts), where f collects the
+fp32 work.  A score is an fp32 sum of 128 exact products: off by at most
+128 * 2^-24 sum |q_i k_i| =: e (scaled).  It enters p as a factor e^{+-2e}
+(numerator and lse), the exponential instruction adds 2^-22, the 2^-24 of
+c x - c m adds |c x| 2^-23, and the sums over n keys add n 2^-24 each at worst,
+so f <= A (4 e + 2^-21 + |s| 2^-22 + n 2^-23) with |s| the largest score.
+"""
+import torch
+
+D = 128
+BF16 = torch.finfo(torch.bfloat16).eps / 2
+
+
+def attention64(q, k, v, past, scale):
+    """q [n, H, D] behind `past` of the keys k, v [past + n, Hkv, D], all on
+    the GPU.  Returns (out, lse, A, smax, e): A as above per element, smax
+    the largest |score| and e the bound of a score's fp32 error, per row."""
+    n, H, _ = q.shape
+    m, Hkv, _ = k.shape
+    G = H // Hkv
+    rows = torch.arange(n, device=q.device)[:, None] + past
+    seen = torch.arange(m, device=q.device)[None, :] <= rows
+    out, A = (torch.empty(n, H, D, dtype=torch.float64, device=q.device) for _ in range(2))
+    lse, smax, e = (torch.empty(n, H, dtype=torch.float64, device=q.device) for _ in range(3))
+    for h in range(H):
+        q64, k64, v64 = q[:, h].double(), k[:, h // G].double(), v[:, h // G].double()
+        x = (q64 @ k64.T) * scale
+        mag = (q64.abs() @ k64.abs().T) * scale
+        x = x.masked_fill(~seen, float("-inf"))
+        lse[:, h] = torch.logsumexp(x, 1)
+        p = torch.exp(x - lse[:, h, None])
+        out[:, h], A[:, h] = p @ v64, p @ v64.abs()
+        smax[:, h] = x.masked_fill(~seen, 0).abs().amax(1)
+        e[:, h] = mag.masked_fill(~seen, 0).amax(1) * 128 * 2.0 ** -24
+    return out, lse, A, smax, e
+
+
+def check(out, lse, ref, keys, what="", p_step=BF16, out_step=BF16):
+    """out [n, H, D], lse [n, H] or None against attention64's `ref`; `keys`:
+    the longest row.  p_step, out_step: half steps of the weights and outputs."""
+    r_out, r_lse, A, smax, e = ref
+    f = 4 * e + 2.0 ** -21 + smax * 2.0 ** -22 + keys * 2.0 ** -23
+    assert torch.isfinite(out).all(), what
+    tol = out_step * r_out.abs() + A * (p_step + f[..., None]) * (1 + out_step) + 1e-30
+    over = ((out.double() - r_out).abs() / tol).max().item() if out.numel() else 0.0
+    assert over <= 1, f"{what}: out off by {over:.2f} of its bound"
+    if lse is not None:
+        # the sum's relative error (as f), the log's and the product's roundings
+        tol = f + (smax + r_lse.abs() + 1) * 2.0 ** -21
+        over = ((lse.double() - r_lse).abs() / tol).max().item() if lse.numel() else 0.0
+        assert over <= 1, f"{what}: lse off by {over:.2f} of its bound"
+
+
+def packed(lens, H, Hkv, seed, device="cuda", scale=1.5):
+    g = torch.Generator(device=device).manual_seed(seed)
+    T = sum(lens)
+    q = torch.randn(T, H, D, generator=g, device=device, dtype=torch.bfloat16) * scale
+    k, v = (torch.randn(T, Hkv, D, generator=g, device=device, dtype=torch.bfloat16) for _ in range(2))
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    return q, k, v, cu, torch.tensor(cu, dtype=torch.int32, device=device)
