@@ -429,6 +429,70 @@ LA_API la_status la_softmax_prefill_varlen(const void *q, const void *k, const v
                                            size_t ws_bytes, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Softmax attention on a paged key/value cache.
+ *
+ * A cache is a pair of device bf16 tensors [n_pages, Hkv, page_size, d]
+ * (page_size 16, 32, 64 or 128): one page holds page_size tokens of all
+ * key/value heads, each head's tokens end to end.  Row b of page_table
+ * (DEVICE int32 [.., max_pages]) lists the pages of request b in order;
+ * cache_lens (DEVICE int32) holds the tokens cached BEFORE the call.  New
+ * tokens are written at positions cache_lens[b], cache_lens[b] + 1, ...; the
+ * table must already name the pages that they fall into, and no other request
+ * of the call may name a page that is written.  The lengths themselves are
+ * the caller's to advance.  What lies in a page behind the last token does not
+ * matter and is not changed.
+ * A page number outside [0, n_pages) that a request needs records
+ * LA_ERR_INVALID_ARGUMENT in the sticky word; nothing outside the pool is
+ * read or written, and that request's outputs are then undefined.
+ *
+ * la_softmax_prefill_paged: la_softmax_prefill_varlen for chunks of prompts.
+ *   The packed new tokens q, k, v of sequence i go behind its cached ones and
+ *   attend to all of them and, causally, to each other.  A sequence without
+ *   new tokens is skipped.  A cache_lens below 0, or one that with the new
+ *   tokens passes max_pages * page_size, refuses the whole call as a bad
+ *   cu_seqlens does: nothing is computed or written, and
+ *   LA_ERR_INVALID_ARGUMENT is recorded.
+ * la_softmax_decode_paged: one new token per request, q [B, H, d] and k, v
+ *   [B, Hkv, d], fused with the cache's update.  out is bf16 or fp32.  A
+ *   cache_lens of -1 marks a row without a request (a padded batch): its
+ *   outputs are left as they are.  One below -1, or that leaves no room for
+ *   the new token, does the same and records LA_ERR_INVALID_ARGUMENT.
+ *   The step reads the keys of all requests in equal shares per SM, so it
+ *   needs no lengths on the host.  The result does not depend on timing.
+ * la_cache_copy_pages: page src[i] is copied to page dst[i] in both tensors,
+ *   i < n (DEVICE int32).  Forks copy their ragged last page, compactions
+ *   move pages to lower numbers.  A destination must not occur twice nor be
+ *   a source of the same call (the pages' contents are then undefined; nothing
+ *   checks it).  A number outside the pool skips its copy and records
+ *   LA_ERR_INVALID_ARGUMENT.
+ * Otherwise arguments, asynchrony and errors are as above; the caches must
+ * not overlap the other buffers.
+ * ------------------------------------------------------------------------- */
+LA_API size_t la_softmax_prefill_paged_workspace_size(int nseq, int total_tokens, int H, int Hkv,
+                                                      int d);
+
+LA_API la_status la_softmax_prefill_paged(const void *q, const void *k, const void *v,
+                                          const int *cu_seqlens, int nseq, int total_tokens,
+                                          int max_seqlen, int H, int Hkv, int d, float scale,
+                                          void *k_cache, void *v_cache, int n_pages, int page_size,
+                                          const int *page_table, int max_pages,
+                                          const int *cache_lens, void *out, float *lse,
+                                          void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+LA_API size_t la_softmax_decode_paged_workspace_size(int B, int H, int Hkv, int d);
+
+LA_API la_status la_softmax_decode_paged(const void *q, const void *k, const void *v, int B, int H,
+                                         int Hkv, int d, float scale, void *k_cache, void *v_cache,
+                                         int n_pages, int page_size, const int *page_table,
+                                         int max_pages, const int *cache_lens, void *out,
+                                         la_dtype out_dtype, float *lse, void *workspace,
+                                         size_t ws_bytes, cudaStream_t stream);
+
+LA_API la_status la_cache_copy_pages(void *k_cache, void *v_cache, int n_pages, int page_size,
+                                     int Hkv, int d, const int *src, const int *dst, int n,
+                                     cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Status.
  * la_get_device_status synchronises `stream`, then returns and clears the
  * sticky device word of the current device (LA_ERR_TIMEOUT,

@@ -29,7 +29,9 @@ EXPORTED = ("la_prefill_workspace_size", "la_prefill", "la_prefill_varlen_worksp
             "la_prefill_backward_workspace_size", "la_prefill_backward", "la_prefill_decay",
             "la_prefill_varlen_decay", "la_decode_step_decay", "la_prefill_from_host_buffer_size",
             "la_prefill_from_host", "la_prefill_backward_varlen_workspace_size", "la_prefill_backward_varlen",
-            "la_softmax_prefill_varlen_workspace_size", "la_softmax_prefill_varlen")
+            "la_softmax_prefill_varlen_workspace_size", "la_softmax_prefill_varlen",
+            "la_softmax_prefill_paged_workspace_size", "la_softmax_prefill_paged",
+            "la_softmax_decode_paged_workspace_size", "la_softmax_decode_paged", "la_cache_copy_pages")
 
 
 class LAError(RuntimeError):
@@ -113,6 +115,18 @@ def lib():
         L.la_softmax_prefill_varlen.argtypes = [vp, vp, vp, vp, c_int, c_int, c_int, c_int, c_int, c_int, f32, vp, vp,
                                                 vp, sz, vp]
         L.la_softmax_prefill_varlen.restype = c_int
+        L.la_softmax_prefill_paged_workspace_size.argtypes = [c_int] * 5
+        L.la_softmax_prefill_paged_workspace_size.restype = sz
+        L.la_softmax_prefill_paged.argtypes = [vp, vp, vp, vp, c_int, c_int, c_int, c_int, c_int, c_int, f32, vp, vp,
+                                               c_int, c_int, vp, c_int, vp, vp, vp, vp, sz, vp]
+        L.la_softmax_prefill_paged.restype = c_int
+        L.la_softmax_decode_paged_workspace_size.argtypes = [c_int] * 4
+        L.la_softmax_decode_paged_workspace_size.restype = sz
+        L.la_softmax_decode_paged.argtypes = [vp, vp, vp, c_int, c_int, c_int, c_int, f32, vp, vp, c_int, c_int, vp,
+                                              c_int, vp, vp, c_int, vp, vp, sz, vp]
+        L.la_softmax_decode_paged.restype = c_int
+        L.la_cache_copy_pages.argtypes = [vp, vp, c_int, c_int, c_int, c_int, vp, vp, c_int, vp]
+        L.la_cache_copy_pages.restype = c_int
         L.la_get_device_status.argtypes = [vp]
         L.la_get_device_status.restype = c_int
         L.la_status_string.argtypes = [c_int]

@@ -5,7 +5,7 @@
 
 namespace {
 
-SmemAttr g_attr_softmax;
+SmemAttr g_attr_softmax, g_attr_softmax_decode;
 
 struct SoftmaxLayout {
     size_t hdr, prefix, entries, total;
@@ -53,6 +53,7 @@ bool encode_page_map(CUtensorMap *map, const void *base, long long rows, int box
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A paged cache as the entry points take it.
 struct PagedCache {
     void *k, *v;
     int n_pages, page;
@@ -61,9 +62,47 @@ struct PagedCache {
     const int *lens;
 };
 
+size_t cache_bytes(const PagedCache &c, int Hkv) { return (size_t)c.n_pages * Hkv * c.page * la::D * 2; }
+
+bool page_size_built(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+
+int log2_of(int x) {
+    int s = 0;
+    while ((1 << s) < x) ++s;
+    return s;
+}
+
+la_status check_cache(const PagedCache &c, int Hkv) {
+    if (c.n_pages <= 0 || c.max_pages <= 0 || c.page <= 0) return LA_ERR_INVALID_ARGUMENT;
+    if (!page_size_built(c.page)) return LA_ERR_UNSUPPORTED;
+    if (!c.k || !c.v || !c.table || !c.lens) return LA_ERR_INVALID_ARGUMENT;
+    if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.table, 4) || !aligned(c.lens, 4))
+        return LA_ERR_INVALID_ARGUMENT;
+    // rows of the cache are tensor-map coordinates
+    if ((long long)c.n_pages * Hkv * c.page > 0x7fffffffLL || (long long)c.max_pages * c.page > 0x7fffffffLL)
+        return LA_ERR_UNSUPPORTED;
+    const size_t n = cache_bytes(c, Hkv);
+    return ranges_overlap(c.k, n, c.v, n) ? LA_ERR_INVALID_ARGUMENT : LA_OK;
+}
+
+// Is the written range [w, w + n) clear of q, k, v and (with one) the cache?
+struct SoftmaxInputs {
+    const void *q, *k, *v;
+    size_t n_q, n_kv;
+    const PagedCache *cache;
+    size_t n_cache;
+};
+
+bool clear_of(const void *w, size_t n, const SoftmaxInputs &in) {
+    if (ranges_overlap(w, n, in.q, in.n_q) || ranges_overlap(w, n, in.k, in.n_kv) || ranges_overlap(w, n, in.v, in.n_kv))
+        return false;
+    return !in.cache || (!ranges_overlap(w, n, in.cache->k, in.n_cache) && !ranges_overlap(w, n, in.cache->v, in.n_cache));
+}
+
+// Shared body of la_softmax_prefill_varlen and, with a cache, la_softmax_prefill_paged.
 la_status softmax_prefill_impl(const void *q, const void *k, const void *v, const int *cu, int nseq, long long T,
-                               int max_seqlen, int H, int Hkv, int d, float scale, void *out, float *lse,
-                               void *workspace, size_t ws_bytes, cudaStream_t stream) {
+                               int max_seqlen, int H, int Hkv, int d, float scale, const PagedCache *cache, void *out,
+                               float *lse, void *workspace, size_t ws_bytes, cudaStream_t stream) {
     la_status st = check_softmax(H, Hkv, d, scale);
     if (st != LA_OK) return st;
     if (nseq < 0 || T < 0 || max_seqlen < 0) return LA_ERR_INVALID_ARGUMENT;
@@ -74,29 +113,35 @@ la_status softmax_prefill_impl(const void *q, const void *k, const void *v, cons
     for (const void *p : ptrs)
         if (p && !aligned(p, 16)) return LA_ERR_INVALID_ARGUMENT;
     if (lse && !aligned(lse, 4)) return LA_ERR_INVALID_ARGUMENT;
+    if (cache && (st = check_cache(*cache, Hkv)) != LA_OK) return st;
     const size_t n_q = (size_t)T * H * la::D * 2, n_kv = (size_t)T * Hkv * la::D * 2, n_lse = (size_t)T * H * 4;
-    if (ranges_overlap(out, n_q, q, n_q) || ranges_overlap(out, n_q, k, n_kv) || ranges_overlap(out, n_q, v, n_kv) ||
-        ranges_overlap(lse, n_lse, q, n_q) || ranges_overlap(lse, n_lse, k, n_kv) ||
-        ranges_overlap(lse, n_lse, v, n_kv) || ranges_overlap(lse, n_lse, out, n_q))
+    const SoftmaxInputs in = {q, k, v, n_q, n_kv, cache, cache ? cache_bytes(*cache, Hkv) : 0};
+    if (!clear_of(out, n_q, in) || !clear_of(lse, n_lse, in) || ranges_overlap(lse, n_lse, out, n_q))
+        return LA_ERR_INVALID_ARGUMENT;
+    if (cache && (ranges_overlap(cache->k, in.n_cache, q, n_q) || ranges_overlap(cache->k, in.n_cache, k, n_kv) ||
+                  ranges_overlap(cache->k, in.n_cache, v, n_kv) || ranges_overlap(cache->v, in.n_cache, q, n_q) ||
+                  ranges_overlap(cache->v, in.n_cache, k, n_kv) || ranges_overlap(cache->v, in.n_cache, v, n_kv)))
         return LA_ERR_INVALID_ARGUMENT;
     const SoftmaxLayout w = softmax_layout(nseq, T);
     if (!workspace || ws_bytes < w.total) return LA_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return LA_ERR_INVALID_ARGUMENT;
-    if (ranges_overlap(workspace, w.total, out, n_q) || ranges_overlap(workspace, w.total, lse, n_lse))
+    if (!clear_of(workspace, w.total, in) || ranges_overlap(workspace, w.total, out, n_q) ||
+        ranges_overlap(workspace, w.total, lse, n_lse))
         return LA_ERR_INVALID_ARGUMENT;
     const int G = H / Hkv, rows = G % 2 ? 2 * la::BLK : la::BLK, pairs = G % 2 ? G : G / 2;
-    if (w.emax * Hkv * (long long)pairs > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
+    const long long items = w.emax * Hkv * (long long)pairs;
+    if (items > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
     int *status = status_word();
     if (!status) return LA_ERR_CUDA;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
 
     la::SoftmaxScheduleParams sp;
     sp.cu = cu;
-    sp.past = nullptr;
+    sp.past = cache ? cache->lens : nullptr;
     sp.nseq = nseq;
     sp.T = (int)T;
     sp.max_seqlen = max_seqlen;
-    sp.max_keys = 0;
+    sp.max_keys = cache ? (long long)cache->max_pages * cache->page : 0;
     sp.rows = rows;
     sp.items_per_entry = Hkv * pairs;
     sp.hdr = reinterpret_cast<int *>(ws + w.hdr);
@@ -109,11 +154,44 @@ la_status softmax_prefill_impl(const void *q, const void *k, const void *v, cons
     if (T == 0) return LA_OK;
 
     CUtensorMap mq, mk, mv;
-    if (!encode_qkv_map(&mq, q, (int)T, H) || !encode_qkv_map(&mk, k, (int)T, Hkv) ||
-        !encode_qkv_map(&mv, v, (int)T, Hkv))
-        return LA_ERR_CUDA;
+    if (!encode_qkv_map(&mq, q, (int)T, H)) return LA_ERR_CUDA;
     la::SoftmaxPrefillParams pp;
     memset(&pp, 0, sizeof pp);
+    if (cache) {
+        const long long cache_rows = (long long)cache->n_pages * Hkv * cache->page;
+        if (!encode_page_map(&mk, cache->k, cache_rows, cache->page) ||
+            !encode_page_map(&mv, cache->v, cache_rows, cache->page))
+            return LA_ERR_CUDA;
+        la::CacheAppendParams ap;
+        ap.k = static_cast<const __nv_bfloat16 *>(k);
+        ap.v = static_cast<const __nv_bfloat16 *>(v);
+        ap.kc = static_cast<__nv_bfloat16 *>(cache->k);
+        ap.vc = static_cast<__nv_bfloat16 *>(cache->v);
+        ap.cu = cu;
+        ap.pages = cache->table;
+        ap.lens = cache->lens;
+        ap.hdr = sp.hdr;
+        ap.nseq = nseq;
+        ap.T = (int)T;
+        ap.Hkv = Hkv;
+        ap.max_pages = cache->max_pages;
+        ap.n_pages = cache->n_pages;
+        ap.page = cache->page;
+        ap.page_shift = log2_of(cache->page);
+        ap.status = status;
+        const long long blocks = (T * Hkv * (la::D / 8) + la::APPEND_THREADS - 1) / la::APPEND_THREADS;
+        la::la_cache_append_kernel<<<(unsigned)(blocks < 148 * 8 ? blocks : 148 * 8), la::APPEND_THREADS, 0, stream>>>(ap);
+        if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
+        ++g_launches;
+        pp.past = cache->lens;
+        pp.pages = cache->table;
+        pp.max_pages = cache->max_pages;
+        pp.n_pages = cache->n_pages;
+        pp.page = cache->page;
+        pp.page_shift = ap.page_shift;
+    } else if (!encode_qkv_map(&mk, k, (int)T, Hkv) || !encode_qkv_map(&mv, v, (int)T, Hkv)) {
+        return LA_ERR_CUDA;
+    }
     pp.out = static_cast<__nv_bfloat16 *>(out);
     pp.lse = lse;
     pp.hdr = sp.hdr;
@@ -126,7 +204,6 @@ la_status softmax_prefill_impl(const void *q, const void *k, const void *v, cons
     pp.scale_log2 = scale * kLog2e;
     pp.wait_limit_ns = g_wait_limit_ns.load();
     pp.status = status;
-    const long long items = w.emax * Hkv * (long long)pairs;
     const int grid = (int)(items < device_sm_count() ? items : device_sm_count());
     st = ensure_smem_attr(g_attr_softmax, la::la_softmax_prefill_kernel, la::SMX_SMEM);
     if (st != LA_OK) return st;
@@ -135,6 +212,25 @@ la_status softmax_prefill_impl(const void *q, const void *k, const void *v, cons
     ++g_launches;
     return LA_OK;
 }
+
+// Launch a kernel that may be set up while the one before it in the stream
+// still runs (it waits for that one's end itself, with griddepcontrol.wait).
+template <class... P, class... A>
+bool launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
+constexpr size_t kDecodeParts = (size_t)la::SD_CTAS * 2 * la::SD_PART * sizeof(float);
+constexpr size_t kDecodeWs = kDecodeParts + (size_t)la::SD_CTAS * sizeof(int4);
 
 }  // namespace
 
@@ -146,6 +242,121 @@ size_t la_softmax_prefill_varlen_workspace_size(int nseq, int total_tokens, int 
 la_status la_softmax_prefill_varlen(const void *q, const void *k, const void *v, const int *cu_seqlens, int nseq,
                                     int total_tokens, int max_seqlen, int H, int Hkv, int d, float scale, void *out,
                                     float *lse, void *workspace, size_t ws_bytes, cudaStream_t stream) {
-    return softmax_prefill_impl(q, k, v, cu_seqlens, nseq, total_tokens, max_seqlen, H, Hkv, d, scale, out, lse,
-                                workspace, ws_bytes, stream);
+    return softmax_prefill_impl(q, k, v, cu_seqlens, nseq, total_tokens, max_seqlen, H, Hkv, d, scale, nullptr, out,
+                                lse, workspace, ws_bytes, stream);
+}
+
+size_t la_softmax_prefill_paged_workspace_size(int nseq, int total_tokens, int H, int Hkv, int d) {
+    return la_softmax_prefill_varlen_workspace_size(nseq, total_tokens, H, Hkv, d);
+}
+
+la_status la_softmax_prefill_paged(const void *q, const void *k, const void *v, const int *cu_seqlens, int nseq,
+                                   int total_tokens, int max_seqlen, int H, int Hkv, int d, float scale,
+                                   void *k_cache, void *v_cache, int n_pages, int page_size, const int *page_table,
+                                   int max_pages, const int *cache_lens, void *out, float *lse, void *workspace,
+                                   size_t ws_bytes, cudaStream_t stream) {
+    const PagedCache cache = {k_cache, v_cache, n_pages, page_size, page_table, max_pages, cache_lens};
+    return softmax_prefill_impl(q, k, v, cu_seqlens, nseq, total_tokens, max_seqlen, H, Hkv, d, scale, &cache, out,
+                                lse, workspace, ws_bytes, stream);
+}
+
+size_t la_softmax_decode_paged_workspace_size(int B, int H, int Hkv, int d) {
+    if (B < 0 || check_softmax(H, Hkv, d, 1.f) != LA_OK) return 0;
+    return kDecodeWs;
+}
+
+la_status la_softmax_decode_paged(const void *q, const void *k, const void *v, int B, int H, int Hkv, int d,
+                                  float scale, void *k_cache, void *v_cache, int n_pages, int page_size,
+                                  const int *page_table, int max_pages, const int *cache_lens, void *out,
+                                  la_dtype out_dtype, float *lse, void *workspace, size_t ws_bytes,
+                                  cudaStream_t stream) {
+    la_status st = check_softmax(H, Hkv, d, scale);
+    if (st != LA_OK) return st;
+    if (B < 0 || (out_dtype != LA_BF16 && out_dtype != LA_FP32)) return LA_ERR_INVALID_ARGUMENT;
+    if (B == 0) return LA_OK;
+    if (!q || !k || !v || !out) return LA_ERR_INVALID_ARGUMENT;
+    const void *ptrs[4] = {q, k, v, out};
+    for (const void *p : ptrs)
+        if (!aligned(p, 16)) return LA_ERR_INVALID_ARGUMENT;
+    if (lse && !aligned(lse, 4)) return LA_ERR_INVALID_ARGUMENT;
+    const PagedCache cache = {k_cache, v_cache, n_pages, page_size, page_table, max_pages, cache_lens};
+    if ((st = check_cache(cache, Hkv)) != LA_OK) return st;
+    const size_t esz = out_dtype == LA_FP32 ? 4 : 2;
+    const size_t n_q = (size_t)B * H * la::D * 2, n_kv = (size_t)B * Hkv * la::D * 2, n_lse = (size_t)B * H * 4;
+    const size_t n_out = (size_t)B * H * la::D * esz;
+    const SoftmaxInputs in = {q, k, v, n_q, n_kv, &cache, cache_bytes(cache, Hkv)};
+    if (!clear_of(out, n_out, in) || !clear_of(lse, n_lse, in) || ranges_overlap(lse, n_lse, out, n_out) ||
+        !clear_of(cache.k, in.n_cache, {q, k, v, n_q, n_kv, nullptr, 0}) ||
+        !clear_of(cache.v, in.n_cache, {q, k, v, n_q, n_kv, nullptr, 0}))
+        return LA_ERR_INVALID_ARGUMENT;
+    if (!workspace || ws_bytes < kDecodeWs) return LA_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return LA_ERR_INVALID_ARGUMENT;
+    if (!clear_of(workspace, kDecodeWs, in) || ranges_overlap(workspace, kDecodeWs, out, n_out) ||
+        ranges_overlap(workspace, kDecodeWs, lse, n_lse))
+        return LA_ERR_INVALID_ARGUMENT;
+    int *status = status_word();
+    if (!status) return LA_ERR_CUDA;
+    const long long cache_rows = (long long)n_pages * Hkv * page_size;
+    const int box = page_size < la::SD_KEYS ? page_size : la::SD_KEYS;
+    CUtensorMap mk, mv;
+    if (!encode_page_map(&mk, k_cache, cache_rows, box) || !encode_page_map(&mv, v_cache, cache_rows, box))
+        return LA_ERR_CUDA;
+    la::SoftmaxDecodeParams dp;
+    dp.q = static_cast<const __nv_bfloat16 *>(q);
+    dp.k = static_cast<const __nv_bfloat16 *>(k);
+    dp.v = static_cast<const __nv_bfloat16 *>(v);
+    dp.kc = static_cast<__nv_bfloat16 *>(k_cache);
+    dp.vc = static_cast<__nv_bfloat16 *>(v_cache);
+    dp.pages = page_table;
+    dp.lens = cache_lens;
+    dp.out = out;
+    dp.lse = lse;
+    dp.parts = static_cast<float *>(workspace);
+    dp.info = reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace) + kDecodeParts);
+    dp.out_fp32 = out_dtype == LA_FP32;
+    dp.B = B;
+    dp.H = H;
+    dp.Hkv = Hkv;
+    dp.G = H / Hkv;
+    dp.chunks = (dp.G + la::SD_HEADS - 1) / la::SD_HEADS;
+    dp.max_pages = max_pages;
+    dp.n_pages = n_pages;
+    dp.page = page_size;
+    dp.page_shift = log2_of(page_size);
+    dp.max_keys = (long long)max_pages * page_size;
+    dp.scale_log2 = scale * kLog2e;
+    dp.wait_limit_ns = g_wait_limit_ns.load();
+    dp.status = status;
+    st = ensure_smem_attr(g_attr_softmax_decode, la::la_softmax_decode_kernel, la::SD_SMEM);
+    if (st != LA_OK) return st;
+    la::la_softmax_decode_kernel<<<la::SD_CTAS, la::SD_THREADS, la::SD_SMEM, stream>>>(mk, mv, dp);
+    if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
+    ++g_launches;
+    if (!launch_dependent(la::la_softmax_join_kernel, dim3(la::SD_CTAS, dp.G < la::SD_HEADS ? dp.G : la::SD_HEADS),
+                          la::D, stream, dp))
+        return LA_ERR_CUDA;
+    ++g_launches;
+    return LA_OK;
+}
+
+la_status la_cache_copy_pages(void *k_cache, void *v_cache, int n_pages, int page_size, int Hkv, int d,
+                              const int *src, const int *dst, int n, cudaStream_t stream) {
+    if (n_pages <= 0 || page_size <= 0 || Hkv <= 0 || d <= 0 || n < 0) return LA_ERR_INVALID_ARGUMENT;
+    if (d != la::D || !page_size_built(page_size)) return LA_ERR_UNSUPPORTED;
+    if (n == 0) return LA_OK;
+    if (!k_cache || !v_cache || !src || !dst || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(src, 4) ||
+        !aligned(dst, 4))
+        return LA_ERR_INVALID_ARGUMENT;
+    const size_t page_bytes = (size_t)Hkv * page_size * la::D * 2, bytes = page_bytes * n_pages;
+    if (ranges_overlap(k_cache, bytes, v_cache, bytes)) return LA_ERR_INVALID_ARGUMENT;
+    int *status = status_word();
+    if (!status) return LA_ERR_CUDA;
+    const long long pieces = (long long)((page_bytes + la::COPY_PIECE - 1) / la::COPY_PIECE);
+    const long long blocks = 2 * pieces * n, most = 148 * 16;
+    la::la_cache_copy_kernel<<<(unsigned)(blocks < most ? blocks : most), la::COPY_THREADS, 0, stream>>>(
+        static_cast<uint8_t *>(k_cache), static_cast<uint8_t *>(v_cache), src, dst, n, n_pages, (long long)page_bytes,
+        status);
+    if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
+    ++g_launches;
+    return LA_OK;
 }

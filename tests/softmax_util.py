@@ -68,3 +68,41 @@ def packed(lens, H, Hkv, seed, device="cuda", scale=1.5):
     for n in lens:
         cu.append(cu[-1] + n)
     return q, k, v, cu, torch.tensor(cu, dtype=torch.int32, device=device)
+
+
+class Cache:
+    """A paged cache of requests with `past` cached tokens and room for `new`
+    more: pages in random order, NaN in every row that holds no token."""
+
+    def __init__(self, past, new, Hkv, page, seed, spare=3):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        need = [-(-(a + b) // page) for a, b in zip(past, new)]
+        self.n_pages = sum(need) + spare
+        ids = torch.randperm(self.n_pages, generator=g, device="cuda").to(torch.int32)
+        # entries behind a request's pages are out of range: they must not be read
+        self.table = torch.full((len(past), max(need + [1])), 1 << 30, dtype=torch.int32, device="cuda")
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = ids[at:at + n]
+            at += n
+        shape = (self.n_pages, Hkv, page, D)
+        self.k, self.v = (torch.full(shape, float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        self.page = page
+        self.past = [torch.randn(2, n, Hkv, D, generator=g, device="cuda", dtype=torch.bfloat16) for n in past]
+        for b, n in enumerate(past):
+            self.write(b, 0, self.past[b][0], self.past[b][1])
+        self.lens = torch.tensor(past, dtype=torch.int32, device="cuda")
+
+    def rows(self, b, n):
+        pos = torch.arange(n, device="cuda")
+        return self.table[b, pos // self.page].long(), pos % self.page
+
+    def write(self, b, at, k, v):
+        pos = torch.arange(at, at + k.shape[0], device="cuda")
+        pid = self.table[b, pos // self.page].long()
+        self.k[pid, :, pos % self.page] = k
+        self.v[pid, :, pos % self.page] = v
+
+    def read(self, b, n):
+        pid, off = self.rows(b, n)
+        return self.k[pid, :, off], self.v[pid, :, off]
