@@ -428,6 +428,30 @@ LA_API la_status la_softmax_prefill_varlen(const void *q, const void *k, const v
                                            void *out, float *lse, void *workspace,
                                            size_t ws_bytes, cudaStream_t stream);
 
+/* la_softmax_prefill_backward_varlen: the gradients of out for dL/dout = dout.
+ * With P_ts = exp(scale q_t . k_s - lse_t) and delta_t = dout_t . out_t:
+ *
+ *   dS_ts = P_ts (dout_t . v_s - delta_t)                    (s <= t)
+ *   dq_t  = scale sum_s dS_ts k_s
+ *   dk_s  = scale sum_t dS_ts q_t,   dv_s = sum_t P_ts dout_t
+ *
+ * dk and dv are summed over the query heads of their group, in fp32 and in a
+ * fixed order (no atomics).  out and lse are those of the forward call.  dout,
+ * dq: bf16 [total_tokens, H, d]; dk, dv: bf16 [total_tokens, Hkv, d]; the four
+ * and the workspace (la_softmax_prefill_backward_varlen_workspace_size bytes,
+ * 256-byte aligned) must not overlap the inputs or each other.  The gradient of
+ * lse is not taken.  Otherwise as la_softmax_prefill_varlen. */
+LA_API size_t la_softmax_prefill_backward_varlen_workspace_size(int nseq, int total_tokens, int H,
+                                                                int Hkv, int d);
+
+LA_API la_status la_softmax_prefill_backward_varlen(const void *q, const void *k, const void *v,
+                                                    const void *out, const float *lse,
+                                                    const void *dout, const int *cu_seqlens,
+                                                    int nseq, int total_tokens, int max_seqlen,
+                                                    int H, int Hkv, int d, float scale, void *dq,
+                                                    void *dk, void *dv, void *workspace,
+                                                    size_t ws_bytes, cudaStream_t stream);
+
 /* ---------------------------------------------------------------------------
  * Softmax attention on a paged key/value cache.
  *

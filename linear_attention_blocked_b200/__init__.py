@@ -39,5 +39,5 @@ from .seqpar import (lasp_prefill, lasp_prefill_backward, lasp_prefill_backward_
                      split_tokens)
 from .serving import BatchPlan, plan_batch  # noqa: F401,E402
 from .streaming import make_buffers, prefill_from_host  # noqa: F401,E402
-from .softmax import (cache_copy_pages, softmax_decode_paged, softmax_prefill_paged,  # noqa: F401,E402
-                      softmax_prefill_varlen)
+from .softmax import (cache_copy_pages, softmax_decode_paged, softmax_prefill_backward_varlen,  # noqa: F401,E402
+                      softmax_prefill_paged, softmax_prefill_varlen)

@@ -30,6 +30,7 @@ EXPORTED = ("la_prefill_workspace_size", "la_prefill", "la_prefill_varlen_worksp
             "la_prefill_varlen_decay", "la_decode_step_decay", "la_prefill_from_host_buffer_size",
             "la_prefill_from_host", "la_prefill_backward_varlen_workspace_size", "la_prefill_backward_varlen",
             "la_softmax_prefill_varlen_workspace_size", "la_softmax_prefill_varlen",
+            "la_softmax_prefill_backward_varlen_workspace_size", "la_softmax_prefill_backward_varlen",
             "la_softmax_prefill_paged_workspace_size", "la_softmax_prefill_paged",
             "la_softmax_decode_paged_workspace_size", "la_softmax_decode_paged", "la_cache_copy_pages")
 
@@ -115,6 +116,11 @@ def lib():
         L.la_softmax_prefill_varlen.argtypes = [vp, vp, vp, vp, c_int, c_int, c_int, c_int, c_int, c_int, f32, vp, vp,
                                                 vp, sz, vp]
         L.la_softmax_prefill_varlen.restype = c_int
+        L.la_softmax_prefill_backward_varlen_workspace_size.argtypes = [c_int] * 5
+        L.la_softmax_prefill_backward_varlen_workspace_size.restype = sz
+        L.la_softmax_prefill_backward_varlen.argtypes = [vp, vp, vp, vp, vp, vp, vp, c_int, c_int, c_int, c_int, c_int,
+                                                         c_int, f32, vp, vp, vp, vp, sz, vp]
+        L.la_softmax_prefill_backward_varlen.restype = c_int
         L.la_softmax_prefill_paged_workspace_size.argtypes = [c_int] * 5
         L.la_softmax_prefill_paged_workspace_size.restype = sz
         L.la_softmax_prefill_paged.argtypes = [vp, vp, vp, vp, c_int, c_int, c_int, c_int, c_int, c_int, f32, vp, vp,

@@ -15,6 +15,7 @@
 #include "la_decode.cuh"
 #include "la_prefill.cuh"
 #include "la_softmax.cuh"
+#include "la_softmax_bwd.cuh"
 #include "la_softmax_decode.cuh"
 
 namespace {

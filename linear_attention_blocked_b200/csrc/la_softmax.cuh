@@ -554,6 +554,7 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     uint32_t o[32];
+                    __syncwarp();
                     tmem_ld_wait32(trow + SMX_TM_O + t * 128 + q * 32, o);
                     if (mine) {
                         uint4 *to = reinterpret_cast<uint4 *>(p.out + at * D + q * 32);

@@ -5,7 +5,7 @@
 
 namespace {
 
-SmemAttr g_attr_softmax, g_attr_softmax_decode;
+SmemAttr g_attr_softmax, g_attr_softmax_decode, g_attr_softmax_dkv, g_attr_softmax_dq;
 
 struct SoftmaxLayout {
     size_t hdr, prefix, entries, total;
@@ -356,6 +356,146 @@ la_status la_cache_copy_pages(void *k_cache, void *v_cache, int n_pages, int pag
     la::la_cache_copy_kernel<<<(unsigned)(blocks < most ? blocks : most), la::COPY_THREADS, 0, stream>>>(
         static_cast<uint8_t *>(k_cache), static_cast<uint8_t *>(v_cache), src, dst, n, n_pages, (long long)page_bytes,
         status);
+    if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
+    ++g_launches;
+    return LA_OK;
+}
+
+namespace {
+
+// Workspace of the backward pass: the scheduler's tables, lse2 and delta, and
+// the fp32 sums of dk and dv where several CTAs share a key block.
+struct SoftmaxBwdLayout {
+    SoftmaxLayout tables;
+    size_t lse2, delta, parts, total;
+    int nparts;
+};
+
+SoftmaxBwdLayout softmax_bwd_layout(int nseq, long long T, int H, int Hkv) {
+    SoftmaxBwdLayout w;
+    w.tables = softmax_layout(nseq, T);
+    const size_t rows = round_up((size_t)T * H * sizeof(float), 256);
+    w.lse2 = w.tables.total;
+    w.delta = w.lse2 + rows;
+    w.parts = w.delta + rows;
+    const int G = H / Hkv;
+    const long long items = w.tables.emax * Hkv, want = 8 * 148;
+    w.nparts = 1;
+    while (w.nparts < 4 && 2 * w.nparts <= G && items * w.nparts < want) w.nparts *= 2;
+    w.total = w.parts + (w.nparts > 1 ? (size_t)w.nparts * 2 * T * Hkv * la::D * sizeof(float) : 0);
+    return w;
+}
+
+}  // namespace
+
+size_t la_softmax_prefill_backward_varlen_workspace_size(int nseq, int total_tokens, int H, int Hkv, int d) {
+    if (nseq < 0 || total_tokens < 0 || check_softmax(H, Hkv, d, 1.f) != LA_OK) return 0;
+    return softmax_bwd_layout(nseq, total_tokens, H, Hkv).total;
+}
+
+la_status la_softmax_prefill_backward_varlen(const void *q, const void *k, const void *v, const void *out,
+                                             const float *lse, const void *dout, const int *cu_seqlens, int nseq,
+                                             int total_tokens, int max_seqlen, int H, int Hkv, int d, float scale,
+                                             void *dq, void *dk, void *dv, void *workspace, size_t ws_bytes,
+                                             cudaStream_t stream) {
+    la_status st = check_softmax(H, Hkv, d, scale);
+    if (st != LA_OK) return st;
+    const long long T = total_tokens;
+    if (nseq < 0 || T < 0 || max_seqlen < 0) return LA_ERR_INVALID_ARGUMENT;
+    if (nseq == 0) return T == 0 ? LA_OK : LA_ERR_INVALID_ARGUMENT;
+    if (!cu_seqlens || !aligned(cu_seqlens, 4)) return LA_ERR_INVALID_ARGUMENT;
+    if (T > 0 && (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv)) return LA_ERR_INVALID_ARGUMENT;
+    const void *ptrs[8] = {q, k, v, out, dout, dq, dk, dv};
+    for (const void *p : ptrs)
+        if (p && !aligned(p, 16)) return LA_ERR_INVALID_ARGUMENT;
+    if (lse && !aligned(lse, 4)) return LA_ERR_INVALID_ARGUMENT;
+    const size_t n_q = (size_t)T * H * la::D * 2, n_kv = (size_t)T * Hkv * la::D * 2, n_lse = (size_t)T * H * 4;
+    const SoftmaxBwdLayout w = softmax_bwd_layout(nseq, T, H, Hkv);
+    struct Range {
+        const void *p;
+        size_t n;
+    };
+    const Range ins[6] = {{q, n_q}, {k, n_kv}, {v, n_kv}, {out, n_q}, {lse, n_lse}, {dout, n_q}};
+    const Range outs[4] = {{dq, n_q}, {dk, n_kv}, {dv, n_kv}, {workspace, w.total}};
+    for (int i = 0; i < 4; ++i) {
+        for (const Range &r : ins)
+            if (ranges_overlap(outs[i].p, outs[i].n, r.p, r.n)) return LA_ERR_INVALID_ARGUMENT;
+        for (int j = i + 1; j < 4; ++j)
+            if (ranges_overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return LA_ERR_INVALID_ARGUMENT;
+    }
+    if (!workspace || ws_bytes < w.total) return LA_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return LA_ERR_INVALID_ARGUMENT;
+    if (w.tables.emax * H > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
+    int *status = status_word();
+    if (!status) return LA_ERR_CUDA;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+
+    la::SoftmaxScheduleParams sp;
+    sp.cu = cu_seqlens;
+    sp.past = nullptr;
+    sp.nseq = nseq;
+    sp.T = (int)T;
+    sp.max_seqlen = max_seqlen;
+    sp.max_keys = 0;
+    sp.rows = la::BLK;
+    sp.items_per_entry = 0;  // both kernels count their own
+    sp.hdr = reinterpret_cast<int *>(ws + w.tables.hdr);
+    sp.prefix = reinterpret_cast<int *>(ws + w.tables.prefix);
+    sp.entries = reinterpret_cast<int4 *>(ws + w.tables.entries);
+    sp.status = status;
+    la::la_softmax_schedule_kernel<<<1, la::SCHED_THREADS, 0, stream>>>(sp);
+    if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
+    ++g_launches;
+    if (T == 0) return LA_OK;
+
+    la::SoftmaxBwdParams bp;
+    float *lse2 = reinterpret_cast<float *>(ws + w.lse2), *delta = reinterpret_cast<float *>(ws + w.delta);
+    bp.lse2 = lse2;
+    bp.delta = delta;
+    bp.dq = static_cast<__nv_bfloat16 *>(dq);
+    bp.dk = static_cast<__nv_bfloat16 *>(dk);
+    bp.dv = static_cast<__nv_bfloat16 *>(dv);
+    bp.parts = w.nparts > 1 ? reinterpret_cast<float *>(ws + w.parts) : nullptr;
+    bp.hdr = sp.hdr;
+    bp.entries = sp.entries;
+    bp.T = (int)T;
+    bp.H = H;
+    bp.Hkv = Hkv;
+    bp.G = H / Hkv;
+    bp.nparts = w.nparts;
+    bp.scale = scale;
+    bp.scale_log2 = scale * kLog2e;
+    bp.wait_limit_ns = g_wait_limit_ns.load();
+    bp.status = status;
+
+    CUtensorMap mq, mk, mv, mg;
+    if (!encode_qkv_map(&mq, q, (int)T, H) || !encode_qkv_map(&mk, k, (int)T, Hkv) ||
+        !encode_qkv_map(&mv, v, (int)T, Hkv) || !encode_qkv_map(&mg, dout, (int)T, H))
+        return LA_ERR_CUDA;
+    const long long row_blocks = (T * H + la::SB_ROWS_THREADS / 16 - 1) / (la::SB_ROWS_THREADS / 16);
+    la::la_softmax_rows_kernel<<<(unsigned)(row_blocks < 148 * 16 ? row_blocks : 148 * 16), la::SB_ROWS_THREADS, 0,
+                                 stream>>>(static_cast<const __nv_bfloat16 *>(out),
+                                           static_cast<const __nv_bfloat16 *>(dout), lse, lse2, delta, (int)T, H);
+    if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
+    ++g_launches;
+
+    if ((st = ensure_smem_attr(g_attr_softmax_dkv, la::la_softmax_dkv_kernel, la::DKV_SMEM)) != LA_OK) return st;
+    if ((st = ensure_smem_attr(g_attr_softmax_dq, la::la_softmax_dq_kernel, la::DQ_SMEM)) != LA_OK) return st;
+    const int sms = device_sm_count();
+    const long long dkv_items = w.tables.emax * Hkv * (long long)w.nparts, dq_items = w.tables.emax * H;
+    la::la_softmax_dkv_kernel<<<(unsigned)(dkv_items < sms ? dkv_items : sms), la::SB_THREADS, la::DKV_SMEM, stream>>>(
+        mq, mk, mv, mg, bp);
+    if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
+    ++g_launches;
+    if (w.nparts > 1) {
+        const long long n = T * Hkv * la::D, blocks = (n / 2 + 255) / 256;
+        la::la_softmax_dkv_sum_kernel<<<(unsigned)(blocks < 148 * 8 ? blocks : 148 * 8), 256, 0, stream>>>(
+            bp.hdr, bp.parts, w.nparts, n, bp.dk, bp.dv);
+        if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
+        ++g_launches;
+    }
+    la::la_softmax_dq_kernel<<<(unsigned)(dq_items < sms ? dq_items : sms), la::SB_THREADS, la::DQ_SMEM, stream>>>(
+        mq, mk, mv, mg, bp);
     if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
     ++g_launches;
     return LA_OK;

@@ -96,6 +96,39 @@ def softmax_prefill_varlen(q, k, v, cu_seqlens, max_seqlen: int, scale=None, out
     return out, lse
 
 
+def softmax_prefill_backward_varlen(q, k, v, out, lse, dout, cu_seqlens, max_seqlen: int, scale=None, dq=None, dk=None,
+                                    dv=None, workspace=None, stream=None):
+    """la_softmax_prefill_backward_varlen: gradients of softmax_prefill_varlen
+    for dL/dout; out and lse are what that call returned, scale what it was
+    given.  Returns (dq [T, H, d], dk, dv [T, Hkv, d]) in bf16."""
+    T, H, Hkv, d = _need_qkv(q, k, v)
+    _need(out, "out", torch.bfloat16, (T, H, d))
+    _need(lse, "lse", torch.float32, (T, H))
+    _need(dout, "dout", torch.bfloat16, (T, H, d))
+    _need(cu_seqlens, "cu_seqlens", torch.int32)
+    nseq = cu_seqlens.numel() - 1
+    if nseq < 0:
+        raise ValueError("cu_seqlens must hold nseq + 1 entries")
+    _same_device(q, k=k, v=v, out=out, lse=lse, dout=dout, cu_seqlens=cu_seqlens, dq=dq, dk=dk, dv=dv,
+                 workspace=workspace)
+    with _on(q, stream) as handle:
+        grads = []
+        for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+            if t is None:
+                t = torch.empty_like(like)
+            _need(t, name, torch.bfloat16, like.shape)
+            grads.append(t)
+        workspace = _workspace(workspace,
+                               lib().la_softmax_prefill_backward_varlen_workspace_size(nseq, T, H, Hkv, d), q.device)
+        st = lib().la_softmax_prefill_backward_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
+                                                      _ptr(cu_seqlens), nseq, T, int(max_seqlen), H, Hkv, d,
+                                                      _scale(scale), _ptr(grads[0]), _ptr(grads[1]), _ptr(grads[2]),
+                                                      _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                                      handle)
+    _check(st, "la_softmax_prefill_backward_varlen")
+    return tuple(grads)
+
+
 def _need_cache(q, k_cache, v_cache, page_table, cache_lens, n, Hkv, d):
     """A paged cache of n requests: (n_pages, page_size, max_pages)."""
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:

@@ -106,3 +106,43 @@ class Cache:
     def read(self, b, n):
         pid, off = self.rows(b, n)
         return self.k[pid, :, off], self.v[pid, :, off]
+
+
+def gradients64(q, k, v, g, scale):
+    """Gradients of one sequence (no past) for dL/dout = g, and bounds of what
+    the kernels' roundings may add to them: {"q": (dq, bound), ...}.
+
+    P is rounded to bf16 once for dv, dS once for dq and dk, and each gradient
+    once: half a step of 2^-8 each.  delta = g . out is formed from the bf16
+    out, which `check` allows to be off by 2^-8 (|out| + A) + f A.  fp32: P is
+    off by a factor of 1 +- r, r = 4 e + 2^-21 + smax 2^-22 as in `check`;
+    g . v and delta are sums of 128 terms; sums over n terms add n 2^-23."""
+    n, H, _ = q.shape
+    Hkv = k.shape[1]
+    G = H // Hkv
+    out, lse, A, smax, e = attention64(q, k, v, 0, scale)
+    seen = torch.ones(n, n, dtype=torch.bool, device=q.device).tril()
+    dq, bq = (torch.zeros(n, H, D, dtype=torch.float64, device=q.device) for _ in range(2))
+    dk, bk, dv, bv = (torch.zeros(n, Hkv, D, dtype=torch.float64, device=q.device) for _ in range(4))
+    u = 2.0 ** -24
+    for h in range(H):
+        q64, k64, v64, g64 = (x.double() for x in (q[:, h], k[:, h // G], v[:, h // G], g[:, h]))
+        p = torch.exp((q64 @ k64.T * scale).masked_fill(~seen, float("-inf")) - lse[:, h, None])
+        r = (4 * e[:, h] + 2.0 ** -21 + smax[:, h] * 2.0 ** -22 + n * 2.0 ** -23)[:, None]
+        o = out[:, h]
+        delta = (g64 * o).sum(1, keepdim=True)
+        dp = g64 @ v64.T
+        ds = p * (dp - delta)
+        o_off = BF16 * o.abs() + A[:, h] * (BF16 + r) * (1 + BF16)
+        off = (g64.abs() * o_off).sum(1, keepdim=True) + 129 * u * (g64.abs() @ v64.abs().T +
+                                                                     (g64 * o).abs().sum(1, keepdim=True))
+        ds_off = ds.abs() * (BF16 + 2 * r) + p * off * (1 + BF16) * (1 + r)
+        p_off = p * (BF16 + 2 * r)
+        dq[:, h] = ds @ k64 * scale
+        bq[:, h] = (ds_off + n * u * 2 * ds.abs()) @ k64.abs() * scale
+        dk[:, h // G] += ds.T @ q64 * scale
+        bk[:, h // G] += (ds_off + n * G * u * 2 * ds.abs()).T @ q64.abs() * scale
+        dv[:, h // G] += p.T @ g64
+        bv[:, h // G] += (p_off + n * G * u * 2 * p).T @ g64.abs()
+    return {name: (x, BF16 * x.abs() + b * (1 + BF16) + 1e-30)
+            for name, x, b in (("q", dq, bq), ("k", dk, bk), ("v", dv, bv))}
