@@ -413,7 +413,7 @@ LA_API la_status la_prefill_backward_varlen(const void *q, const void *k, const 
  *                needs it; with it partial results over disjoint keys can be
  *                joined.
  *   workspace    la_softmax_prefill_varlen_workspace_size bytes, 256-byte
- *                aligned, as for la_prefill.
+ *                aligned, as for la_prefill; NULL will do where that is 0.
  * Scores, maxima, sums and outputs are accumulated in fp32; the weights are
  * rounded to bf16 once for the product with v.  A row depends on its own
  * sequence alone; a value that is not finite in row s of v may reach earlier
@@ -503,7 +503,8 @@ LA_API la_status la_softmax_prefill_paged(const void *q, const void *k, const vo
                                           const int *cache_lens, void *out, float *lse,
                                           void *workspace, size_t ws_bytes, cudaStream_t stream);
 
-LA_API size_t la_softmax_decode_paged_workspace_size(int B, int H, int Hkv, int d);
+LA_API size_t la_softmax_decode_paged_workspace_size(int B, int H, int Hkv, int d, int page_size,
+                                                     int max_pages);
 
 LA_API la_status la_softmax_decode_paged(const void *q, const void *k, const void *v, int B, int H,
                                          int Hkv, int d, float scale, void *k_cache, void *v_cache,

@@ -126,7 +126,7 @@ def lib():
         L.la_softmax_prefill_paged.argtypes = [vp, vp, vp, vp, c_int, c_int, c_int, c_int, c_int, c_int, f32, vp, vp,
                                                c_int, c_int, vp, c_int, vp, vp, vp, vp, sz, vp]
         L.la_softmax_prefill_paged.restype = c_int
-        L.la_softmax_decode_paged_workspace_size.argtypes = [c_int] * 4
+        L.la_softmax_decode_paged_workspace_size.argtypes = [c_int] * 6
         L.la_softmax_decode_paged_workspace_size.restype = sz
         L.la_softmax_decode_paged.argtypes = [vp, vp, vp, c_int, c_int, c_int, c_int, f32, vp, vp, c_int, c_int, vp,
                                               c_int, vp, vp, c_int, vp, vp, sz, vp]

@@ -133,18 +133,20 @@ struct SmemAttr {
     bool done[kMaxDevices] = {};
 };
 
+// cluster16: also allow clusters of 16 CTAs, more than the portable 8.
 template <typename Kernel>
-la_status ensure_smem_attr(SmemAttr &a, Kernel *kernel, int bytes) {
+la_status ensure_smem_attr(SmemAttr &a, Kernel *kernel, int bytes, bool cluster16 = false) {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return LA_ERR_CUDA;
-    if (dev >= kMaxDevices) {  // not cached: set it on every call
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess
-                   ? LA_OK : LA_ERR_CUDA;
-    }
+    auto set = [&]() -> bool {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess &&
+               (!cluster16 ||
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess);
+    };
+    if (dev >= kMaxDevices) return set() ? LA_OK : LA_ERR_CUDA;  // not cached: set it on every call
     std::lock_guard<std::mutex> lock(a.mu);
     if (!a.done[dev]) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-            return LA_ERR_CUDA;
+        if (!set()) return LA_ERR_CUDA;
         a.done[dev] = true;
     }
     return LA_OK;

@@ -32,6 +32,7 @@
 //   warp 0       items and K/V tiles (TMA)         warpgroup 0: 48 registers
 //   warp 1       TMEM allocator + MMA issuer
 //   warp 2       Q tiles (TMA)
+//   warp 3       (small chunks) new tokens into their pages
 //   warps 4-7    softmax of tile 0                 192 registers
 //   warps 8-11   softmax of tile 1                 192 registers
 //   warps 12-15  output: O / l, lse                80 registers
@@ -81,8 +82,16 @@ struct SoftmaxPrefillParams {
     int *hdr;
     const int4 *entries;
     const int *past;          // device [nseq] or null
-    const int *pages;         // device [nseq, max_pages] page table, or null (packed K and V)
+    const int *pages;         // device [nseq, max_pages] page table, or null (no cache)
     int max_pages, n_pages, page, page_shift;
+    // direct: every CTA has one item at most and finds it in cu itself
+    int direct;
+    const int *cu;            // device [nseq + 1] (direct, append)
+    int nseq, T, max_seqlen;
+    long long max_keys;       // room of a sequence's pages
+    // new tokens that this kernel writes into their pages (direct), or null
+    const __nv_bfloat16 *new_k, *new_v;
+    __nv_bfloat16 *kc, *vc;
     int H, Hkv, G;
     int pairs;                // pairs of query tiles per entry
     int rows;
@@ -93,6 +102,8 @@ struct SoftmaxPrefillParams {
 
 // item fields
 enum { SI_VALID = 0, SI_H0, SI_H1, SI_B0, SI_B1, SI_N0, SI_N1, SI_TOK0, SI_LEN, SI_PAST, SI_KVH, SI_SEQ, SI_FIELDS };
+// N0, N1: key tiles of the two query tiles: those of the cached tokens, then those
+// of the new ones up to the query tile's own rows
 
 struct SoftmaxCtrl {
     uint64_t kv_full[SMX_STAGES], kv_empty[SMX_STAGES];
@@ -112,6 +123,11 @@ struct SoftmaxCtrl {
 };
 static_assert(sizeof(SoftmaxCtrl) <= 512, "control block");
 static_assert(SI_FIELDS <= 12, "item fields");
+
+// Programmatic dependent launch: wait for the kernel before this one in the
+// stream to end (when it was launched so; else a no-op); let the next one start.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <int N>
 __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -156,26 +172,17 @@ __device__ __forceinline__ bool smx_next(uint32_t &it, int (&item)[SI_FIELDS], i
     return item[SI_VALID] != 0;
 }
 
-// The item of ticket t: key/value head (outermost, so that the CTAs at work
-// share its keys in L2), entry, pair of tiles.
-__device__ __forceinline__ void smx_item(int t, int ne, const SoftmaxPrefillParams &p, int *item) {
-    const int per_head = ne * p.pairs;
-    const int kvh = t / per_head;
-    const int rest = t - kvh * per_head;
-    const int e = rest / p.pairs, pair = rest - e * p.pairs;
-    const int4 en = p.entries[e];
+// The item of (key/value head, entry, pair of tiles).
+__device__ __forceinline__ void smx_item(int kvh, int4 en, int pair, const SoftmaxPrefillParams &p, int *item) {
     const int past = p.past ? p.past[en.x] : 0;
     const int bpe = p.rows / BLK;  // blocks per entry
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         const int u = 2 * pair + w;
         const int b = en.w * bpe + u / p.G;
-        const int row = b * BLK;
-        // keys that the tile's last row sees
-        const int keys = past + min(row + BLK, en.z);
         item[SI_H0 + w] = kvh * p.G + u % p.G;
         item[SI_B0 + w] = b;
-        item[SI_N0 + w] = (u < bpe * p.G && row < en.z) ? (keys + BLK - 1) / BLK : 0;
+        item[SI_N0 + w] = (u < bpe * p.G && b * BLK < en.z) ? (past + BLK - 1) / BLK + b + 1 : 0;
     }
     item[SI_TOK0] = en.y;
     item[SI_LEN] = en.z;
@@ -184,22 +191,60 @@ __device__ __forceinline__ void smx_item(int t, int ne, const SoftmaxPrefillPara
     item[SI_SEQ] = en.x;
 }
 
-// One K or V tile: rows [row, row + 128) of a packed tensor, or the pages that
-// hold keys [key0, key0 + 128) of a sequence with `keys` of them.  Called by a
-// whole warp; with pages, lane i brings page i of the tile (both halves), and
-// what lies behind the last key is not loaded.
-__device__ __forceinline__ void smx_load_tile(uint8_t *dst, const CUtensorMap *tm, uint64_t *bar, int kvh, int row,
-                                              int key0, int keys, int pid, int lane, uint64_t pol,
-                                              const SoftmaxPrefillParams &p) {
-    if (!p.pages) {
-        if (lane == 0) {
-            mbar_expect_tx(bar, TILE_BYTES);
-            tma_load_4d(dst, tm, bar, 0, kvh, row, 0, pol);
+// Is sequence i of the tables as the header asks?
+__device__ __forceinline__ bool smx_sequence_ok(int i, int a, int b, const int *past, int T, int max_seqlen,
+                                                long long max_keys) {
+    if (a < 0 || b < a || b > T || b - a > max_seqlen) return false;
+    if (!past || b == a) return true;
+    return past[i] >= 0 && (long long)past[i] + (b - a) <= max_keys;
+}
+
+// Entry e by a warp's own walk over cu_seqlens, checking all of it as the
+// scheduler does: its number of entries, 0 when the tables are refused.
+__device__ __forceinline__ int smx_find(int e, int lane, const SoftmaxPrefillParams &p, int4 &en) {
+    int at = 0;
+    bool bad = lane == 0 && (p.cu[0] != 0 || p.cu[p.nseq] != p.T);
+    for (int base = 0; base < p.nseq; base += 32) {
+        const int i = base + lane;
+        int a = 0, b = 0;
+        if (i < p.nseq) {
+            a = p.cu[i];
+            b = p.cu[i + 1];
+            if (!smx_sequence_ok(i, a, b, p.past, p.T, p.max_seqlen, p.max_keys)) {
+                bad = true;
+                b = a;
+            }
         }
-        return;
+        const int n = (b - a + p.rows - 1) / p.rows;
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        const int first = at + x - n;
+        const uint32_t hit = __ballot_sync(0xffffffffu, e >= first && e < first + n);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            en = make_int4(base + src, __shfl_sync(0xffffffffu, a, src), __shfl_sync(0xffffffffu, b - a, src),
+                           __shfl_sync(0xffffffffu, first + n - 1 - e, src));
+        }
+        at += __shfl_sync(0xffffffffu, x, 31);
     }
-    const int left = min(keys - key0, BLK);
-    const int np = (left + p.page - 1) >> p.page_shift;
+    if (__any_sync(0xffffffffu, bad)) {
+        if (lane == 0) record_status(p.status, ST_INVALID);
+        return 0;
+    }
+    return at;
+}
+
+// The pages that hold keys [key0, key0 + 128) of a sequence with `keys` cached
+// ones, as one K or V tile.  Called by a whole warp: lane i brings page i of the
+// tile (both halves); what lies behind the last key's page is not loaded.
+__device__ __forceinline__ void smx_load_pages(uint8_t *dst, const CUtensorMap *tm, uint64_t *bar, int kvh, int key0,
+                                               int keys, int pid, int lane, uint64_t pol,
+                                               const SoftmaxPrefillParams &p) {
+    const int np = (min(keys - key0, BLK) + p.page - 1) >> p.page_shift;
     if (lane == 0) mbar_expect_tx(bar, (uint32_t)(np * p.page * D * 2));
     __syncwarp();
     if (lane < np) {
@@ -210,9 +255,42 @@ __device__ __forceinline__ void smx_load_tile(uint8_t *dst, const CUtensorMap *t
     }
 }
 
+// 16 bytes of k and of v of the new tokens into their pages: piece e of
+// T x Hkv x 16, token t of sequence b going to position past[b] + t.
+struct AppendTables {
+    const __nv_bfloat16 *k, *v;   // [T, Hkv, D]
+    __nv_bfloat16 *kc, *vc;       // [n_pages, Hkv, page, D]
+    const int *cu, *pages, *past;
+    int nseq, Hkv, max_pages, n_pages, page, page_shift;
+    int *status;
+};
+__device__ __forceinline__ void append_piece(long long e, const AppendTables &p) {
+    const int ch = (int)(e % (D / 8));
+    const long long th = e / (D / 8);
+    const int h = (int)(th % p.Hkv), t = (int)(th / p.Hkv);
+    const size_t from = (size_t)th * D + ch * 8;
+    const uint4 kx = *reinterpret_cast<const uint4 *>(p.k + from), vx = *reinterpret_cast<const uint4 *>(p.v + from);
+    int lo = 0, hi = p.nseq - 1;  // the last sequence that starts at or before t
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.cu[mid] <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    const int pos = p.past[lo] + t - p.cu[lo];
+    const int pid = p.pages[(size_t)lo * p.max_pages + (pos >> p.page_shift)];
+    if (pid < 0 || pid >= p.n_pages) {  // nothing outside the pool is written
+        record_status(p.status, ST_INVALID);
+        return;
+    }
+    const size_t to = ((((size_t)pid * p.Hkv + h) << p.page_shift) + (pos & (p.page - 1))) * D + ch * 8;
+    *reinterpret_cast<uint4 *>(p.kc + to) = kx;
+    *reinterpret_cast<uint4 *>(p.vc + to) = vx;
+}
+
 __global__ void __launch_bounds__(SMX_THREADS, 1)
 la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                          const __grid_constant__ CUtensorMap tmv, const __grid_constant__ SoftmaxPrefillParams p) {
+                          const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmkc,
+                          const __grid_constant__ CUtensorMap tmvc, const __grid_constant__ SoftmaxPrefillParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     SoftmaxCtrl *cb = reinterpret_cast<SoftmaxCtrl *>(smem + SMX_CTRL);
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -265,7 +343,16 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
         if (warp == 0) {
             // ===================== items, K and V tiles =====================
             const uint64_t pol = policy_evict_last();
-            const int total = p.hdr[HDR_TOTAL], ne = p.hdr[HDR_G];
+            int total = 0, ne = 0;
+            int4 own = make_int4(0, 0, 0, 0);
+            if (p.direct) {
+                const int e = blockIdx.x / (p.Hkv * p.pairs);
+                total = e < smx_find(e, lane, p, own) ? 1 : 0;
+            } else {
+                pdl_wait();  // the scheduler's tables
+                total = p.hdr[HDR_TOTAL];
+                ne = p.hdr[HDR_G];
+            }
             uint32_t it = 0, n = 0;
             bool ok = true;
             for (;;) {
@@ -273,26 +360,37 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
                 if (!wait(&cb->item_empty[slot], ((it / SMX_SLOTS) & 1) ^ 1)) { ok = false; break; }
                 int t = 0;
                 if (lane == 0) {
-                    t = atomicAdd(&p.hdr[HDR_TICKET], 1);
+                    int kvh, rest;
+                    if (p.direct) {
+                        t = (int)it;
+                        rest = blockIdx.x % (p.Hkv * p.pairs);
+                        kvh = rest / p.pairs;
+                    } else {
+                        // key/value head outermost, so that the CTAs at work share its keys in L2
+                        t = atomicAdd(&p.hdr[HDR_TICKET], 1);
+                        const int per_head = max(1, ne * p.pairs);
+                        kvh = t / per_head;
+                        rest = t - kvh * per_head;
+                        if (t < total) own = p.entries[rest / p.pairs];
+                    }
                     cb->item[slot][SI_VALID] = t < total;
-                    if (t < total) smx_item(t, ne, p, cb->item[slot]);
+                    if (t < total) smx_item(kvh, own, rest % p.pairs, p, cb->item[slot]);
                 }
                 t = __shfl_sync(0xffffffffu, t, 0);
                 __syncwarp();
                 const int n0 = cb->item[slot][SI_N0], n1 = cb->item[slot][SI_N1];
                 const int kvh = cb->item[slot][SI_KVH], tok0 = cb->item[slot][SI_TOK0];
-                const int keys = cb->item[slot][SI_PAST] + cb->item[slot][SI_LEN];
-                const int seq = cb->item[slot][SI_SEQ];
+                const int past = cb->item[slot][SI_PAST], seq = cb->item[slot][SI_SEQ];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&cb->item_full[slot]);
                 ++it;
                 if (t >= total) break;
-                const int nmax = max(n0, n1);
+                const int nmax = max(n0, n1), np = (past + BLK - 1) / BLK;
                 for (int j = 0; j < nmax && ok; ++j) {
                     int pid = 0;
-                    if (p.pages) {
+                    if (j < np) {
                         const int i = (j << (7 - p.page_shift)) + lane;  // page of this lane in the tile
-                        if (lane < (BLK >> p.page_shift) && (i << p.page_shift) < keys) {
+                        if (lane < (BLK >> p.page_shift) && (i << p.page_shift) < past) {
                             pid = p.pages[(size_t)seq * p.max_pages + i];
                             if (pid < 0 || pid >= p.n_pages) {  // nothing outside the pool is read
                                 record_status(p.status, ST_INVALID);
@@ -302,9 +400,14 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
                     }
                     for (int kv = 0; kv < 2; ++kv) {
                         const int s = n % SMX_STAGES;
+                        uint8_t *dst = smem + SMX_KV + s * TILE_BYTES;
                         if (!wait(&cb->kv_empty[s], ((n / SMX_STAGES) & 1) ^ 1)) { ok = false; break; }
-                        smx_load_tile(smem + SMX_KV + s * TILE_BYTES, kv ? &tmv : &tmk, &cb->kv_full[s], kvh,
-                                      tok0 + j * BLK, j * BLK, keys, pid, lane, pol, p);
+                        if (j < np) {
+                            smx_load_pages(dst, kv ? &tmvc : &tmkc, &cb->kv_full[s], kvh, j * BLK, past, pid, lane, pol, p);
+                        } else if (lane == 0) {
+                            mbar_expect_tx(&cb->kv_full[s], TILE_BYTES);
+                            tma_load_4d(dst, kv ? &tmv : &tmk, &cb->kv_full[s], 0, kvh, tok0 + (j - np) * BLK, 0, pol);
+                        }
                         ++n;
                     }
                 }
@@ -350,7 +453,7 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
             };
             while (ok) {
                 const int n0 = cur[SI_N0], n1 = cur[SI_N1], nmax = max(n0, n1);
-                const int keys = cur[SI_PAST] + cur[SI_LEN];
+                const int np = (cur[SI_PAST] + BLK - 1) / BLK;
                 bool have_nxt = false, nxt_valid = false;
                 for (int t = 0; t < 2 && ok; ++t) {
                     if (((pend >> t) & 1) && (t ? n1 : n0) > 0) {
@@ -365,7 +468,7 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
                         const uint32_t pos = base + 2 * j + 1, s = pos % SMX_STAGES;
                         uint8_t *vp = smem + SMX_KV + s * TILE_BYTES;
                         if (!wait(&cb->kv_full[s], (pos / SMX_STAGES) & 1)) { ok = false; break; }
-                        const int valid = keys - j * BLK;
+                        const int valid = j < np ? cur[SI_PAST] - j * BLK : cur[SI_LEN] - (j - np) * BLK;
                         if (valid < BLK && (t == 0 || j >= n0)) {
                             // rows behind the last key meet P = 0, which keeps out what they
                             // hold only if it is finite: zero them
@@ -442,6 +545,18 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
                     int dummy = 0;
                     la_wait(&cb->q_full[t], (n[t] - 1) & 1, globaltimer_ns() + p.wait_limit_ns, &dummy);
                 }
+        } else if (p.new_k) {
+            // ===================== new tokens into their pages =====================
+            // (no CTA reads them there: their tiles come from the packed tensors)
+            int4 unused;
+            if (smx_find(-1, lane, p, unused) > 0) {
+                const AppendTables at = {p.new_k, p.new_v, p.kc, p.vc, p.cu, p.pages, p.past, p.nseq,
+                                         p.Hkv, p.max_pages, p.n_pages, p.page, p.page_shift, p.status};
+                const long long total = (long long)p.T * p.Hkv * (D / 8);
+#pragma unroll 2
+                for (long long e = (long long)blockIdx.x * 32 + lane; e < total; e += (long long)gridDim.x * 32)
+                    append_piece(e, at);
+            }
         }
     } else if (warp < 12) {
         // ===================== softmax of tile t =====================
@@ -459,17 +574,16 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
         while (ok && smx_next<MASK>(it, im, lane, p, cb)) {
             const int nt = t ? im[SI_N1] : im[SI_N0];
             if (nt == 0) continue;
-            const int row = (t ? im[SI_B1] : im[SI_B0]) * BLK;
-            const int pos = im[SI_PAST] + row + r;  // the row's own position among the keys
-            const int first = im[SI_PAST] + row;    // that of the tile's first row
+            const int past = im[SI_PAST], np = (past + BLK - 1) / BLK;
             float m = -INFINITY, l = 0.f;           // m: maximum in use
             for (int j = 0; j < nt; ++j) {
                 if (!wait(&cb->s_full[t], sn & 1)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t x[128];
                 tmem_ld_cols<128>(ts, x);
-                if (j * BLK + BLK - 1 > first) {
-                    const int lim = pos - j * BLK;  // columns [0, lim] are seen
+                // the last tile of cached keys may be ragged, that of the own rows is the diagonal
+                if (j == nt - 1 || (j < np && past - j * BLK < BLK)) {
+                    const int lim = j < np ? past - j * BLK - 1 : r;  // columns [0, lim] are seen
 #pragma unroll
                     for (int i = 0; i < 128; ++i)
                         if (i > lim) x[i] = 0xff800000u;  // -inf
@@ -590,16 +704,11 @@ __global__ void __launch_bounds__(SCHED_THREADS, 1) la_softmax_schedule_kernel(c
     __shared__ int warp_sums[SCHED_THREADS / 32];
     __shared__ int carry_sh;
     const int tid = threadIdx.x;
+    pdl_launch();
     int bad = 0;
     if (tid == 0 && (s.cu[0] != 0 || s.cu[s.nseq] != s.T)) bad = 1;
-    for (int i = tid; i < s.nseq; i += SCHED_THREADS) {
-        const int a = s.cu[i], b = s.cu[i + 1];
-        if (a < 0 || b < a || b > s.T || b - a > s.max_seqlen) bad = 1;
-        if (s.past && b > a) {
-            const int past = s.past[i];
-            if (past < 0 || (long long)past + (b - a) > s.max_keys) bad = 1;
-        }
-    }
+    for (int i = tid; i < s.nseq; i += SCHED_THREADS)
+        if (!smx_sequence_ok(i, s.cu[i], s.cu[i + 1], s.past, s.T, s.max_seqlen, s.max_keys)) bad = 1;
     bad = __syncthreads_or(bad);
     if (tid == 0) {
         s.hdr[HDR_TICKET] = 0;

@@ -5,7 +5,7 @@
 
 namespace {
 
-SmemAttr g_attr_softmax, g_attr_softmax_decode, g_attr_softmax_dkv, g_attr_softmax_dq;
+SmemAttr g_attr_softmax, g_attr_softmax_decode, g_attr_softmax_cluster, g_attr_softmax_cluster16, g_attr_softmax_dkv, g_attr_softmax_dq;
 
 struct SoftmaxLayout {
     size_t hdr, prefix, entries, total;
@@ -24,6 +24,26 @@ SoftmaxLayout softmax_layout(int nseq, long long T) {
     return w;
 }
 
+// Work items of the prompt kernel: pairs of query tiles.  With no more items
+// than SMs every CTA has one at most, which it finds itself: no scheduler launch
+// and no workspace (129 tokens, 64 heads over 8: 14.4 us with, 12.3 us without).
+// Depends on the shape only, so that the workspace size does.
+struct SoftmaxItems {
+    int rows, pairs;   // rows per entry, pairs per entry and key/value head
+    long long items;
+    bool direct;
+};
+
+SoftmaxItems softmax_items(int nseq, long long T, int H, int Hkv) {
+    const int G = H / Hkv;
+    SoftmaxItems s;
+    s.rows = G % 2 ? 2 * la::BLK : la::BLK;
+    s.pairs = G % 2 ? G : G / 2;
+    s.items = (T / s.rows + nseq) * Hkv * s.pairs;
+    s.direct = T > 0 && s.items <= 148;
+    return s;
+}
+
 la_status check_softmax(int H, int Hkv, int d, float scale) {
     if (H <= 0 || Hkv <= 0 || d <= 0 || H % Hkv) return LA_ERR_INVALID_ARGUMENT;
     if (!(scale > 0.f) || scale > 3.0e38f) return LA_ERR_INVALID_ARGUMENT;  // also rejects NaN
@@ -34,8 +54,13 @@ la_status check_softmax(int H, int Hkv, int d, float scale) {
 constexpr float kLog2e = 1.44269504088896341f;
 
 int *status_word() {
+    static std::atomic<int *> cached[kMaxDevices];  // the address is fixed per device
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return nullptr;
+    if (dev < kMaxDevices && cached[dev].load()) return cached[dev].load();
     int *status = nullptr;
     if (cudaGetSymbolAddress(reinterpret_cast<void **>(&status), g_la_status) != cudaSuccess) return nullptr;
+    if (dev < kMaxDevices) cached[dev].store(status);
     return status;
 }
 
@@ -99,6 +124,23 @@ bool clear_of(const void *w, size_t n, const SoftmaxInputs &in) {
     return !in.cache || (!ranges_overlap(w, n, in.cache->k, in.n_cache) && !ranges_overlap(w, n, in.cache->v, in.n_cache));
 }
 
+// Launch a kernel that may be set up while the one before it in the stream
+// still runs (it waits for that one's end itself, with griddepcontrol.wait).
+template <class... P, class... A>
+bool launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
 // Shared body of la_softmax_prefill_varlen and, with a cache, la_softmax_prefill_paged.
 la_status softmax_prefill_impl(const void *q, const void *k, const void *v, const int *cu, int nseq, long long T,
                                int max_seqlen, int H, int Hkv, int d, float scale, const PagedCache *cache, void *out,
@@ -122,75 +164,80 @@ la_status softmax_prefill_impl(const void *q, const void *k, const void *v, cons
                   ranges_overlap(cache->k, in.n_cache, v, n_kv) || ranges_overlap(cache->v, in.n_cache, q, n_q) ||
                   ranges_overlap(cache->v, in.n_cache, k, n_kv) || ranges_overlap(cache->v, in.n_cache, v, n_kv)))
         return LA_ERR_INVALID_ARGUMENT;
+    const SoftmaxItems it = softmax_items(nseq, T, H, Hkv);
     const SoftmaxLayout w = softmax_layout(nseq, T);
-    if (!workspace || ws_bytes < w.total) return LA_ERR_WORKSPACE;
-    if (!aligned(workspace, 256)) return LA_ERR_INVALID_ARGUMENT;
-    if (!clear_of(workspace, w.total, in) || ranges_overlap(workspace, w.total, out, n_q) ||
-        ranges_overlap(workspace, w.total, lse, n_lse))
-        return LA_ERR_INVALID_ARGUMENT;
-    const int G = H / Hkv, rows = G % 2 ? 2 * la::BLK : la::BLK, pairs = G % 2 ? G : G / 2;
-    const long long items = w.emax * Hkv * (long long)pairs;
+    if (!it.direct) {
+        if (!workspace || ws_bytes < w.total) return LA_ERR_WORKSPACE;
+        if (!aligned(workspace, 256)) return LA_ERR_INVALID_ARGUMENT;
+        if (!clear_of(workspace, w.total, in) || ranges_overlap(workspace, w.total, out, n_q) ||
+            ranges_overlap(workspace, w.total, lse, n_lse))
+            return LA_ERR_INVALID_ARGUMENT;
+    }
+    const int G = H / Hkv, rows = it.rows, pairs = it.pairs;
+    const bool direct = it.direct;
+    const long long items = it.items;
     if (items > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
     int *status = status_word();
     if (!status) return LA_ERR_CUDA;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
 
+    const long long max_keys = cache ? (long long)cache->max_pages * cache->page : 0;
+    const int sms = device_sm_count();
     la::SoftmaxScheduleParams sp;
     sp.cu = cu;
     sp.past = cache ? cache->lens : nullptr;
     sp.nseq = nseq;
     sp.T = (int)T;
     sp.max_seqlen = max_seqlen;
-    sp.max_keys = cache ? (long long)cache->max_pages * cache->page : 0;
+    sp.max_keys = max_keys;
     sp.rows = rows;
     sp.items_per_entry = Hkv * pairs;
     sp.hdr = reinterpret_cast<int *>(ws + w.hdr);
     sp.prefix = reinterpret_cast<int *>(ws + w.prefix);
     sp.entries = reinterpret_cast<int4 *>(ws + w.entries);
     sp.status = status;
-    la::la_softmax_schedule_kernel<<<1, la::SCHED_THREADS, 0, stream>>>(sp);
-    if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
-    ++g_launches;
-    if (T == 0) return LA_OK;
+    if (!direct) {  // (without tokens only the tables are checked)
+        la::la_softmax_schedule_kernel<<<1, la::SCHED_THREADS, 0, stream>>>(sp);
+        if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
+        ++g_launches;
+        if (T == 0) return LA_OK;
+    }
 
-    CUtensorMap mq, mk, mv;
-    if (!encode_qkv_map(&mq, q, (int)T, H)) return LA_ERR_CUDA;
+    CUtensorMap mq, mk, mv, mkc, mvc;
+    if (!encode_qkv_map(&mq, q, (int)T, H) || !encode_qkv_map(&mk, k, (int)T, Hkv) ||
+        !encode_qkv_map(&mv, v, (int)T, Hkv))
+        return LA_ERR_CUDA;
     la::SoftmaxPrefillParams pp;
     memset(&pp, 0, sizeof pp);
     if (cache) {
         const long long cache_rows = (long long)cache->n_pages * Hkv * cache->page;
-        if (!encode_page_map(&mk, cache->k, cache_rows, cache->page) ||
-            !encode_page_map(&mv, cache->v, cache_rows, cache->page))
+        if (!encode_page_map(&mkc, cache->k, cache_rows, cache->page) ||
+            !encode_page_map(&mvc, cache->v, cache_rows, cache->page))
             return LA_ERR_CUDA;
-        la::CacheAppendParams ap;
-        ap.k = static_cast<const __nv_bfloat16 *>(k);
-        ap.v = static_cast<const __nv_bfloat16 *>(v);
-        ap.kc = static_cast<__nv_bfloat16 *>(cache->k);
-        ap.vc = static_cast<__nv_bfloat16 *>(cache->v);
-        ap.cu = cu;
-        ap.pages = cache->table;
-        ap.lens = cache->lens;
-        ap.hdr = sp.hdr;
-        ap.nseq = nseq;
-        ap.T = (int)T;
-        ap.Hkv = Hkv;
-        ap.max_pages = cache->max_pages;
-        ap.n_pages = cache->n_pages;
-        ap.page = cache->page;
-        ap.page_shift = log2_of(cache->page);
-        ap.status = status;
-        const long long blocks = (T * Hkv * (la::D / 8) + la::APPEND_THREADS - 1) / la::APPEND_THREADS;
-        la::la_cache_append_kernel<<<(unsigned)(blocks < 148 * 8 ? blocks : 148 * 8), la::APPEND_THREADS, 0, stream>>>(ap);
-        if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
-        ++g_launches;
         pp.past = cache->lens;
         pp.pages = cache->table;
         pp.max_pages = cache->max_pages;
         pp.n_pages = cache->n_pages;
         pp.page = cache->page;
-        pp.page_shift = ap.page_shift;
-    } else if (!encode_qkv_map(&mk, k, (int)T, Hkv) || !encode_qkv_map(&mv, v, (int)T, Hkv)) {
-        return LA_ERR_CUDA;
+        pp.page_shift = log2_of(cache->page);
+        pp.kc = static_cast<__nv_bfloat16 *>(cache->k);
+        pp.vc = static_cast<__nv_bfloat16 *>(cache->v);
+        if (direct) {
+            pp.new_k = static_cast<const __nv_bfloat16 *>(k);
+            pp.new_v = static_cast<const __nv_bfloat16 *>(v);
+        } else {
+            const la::AppendTables at = {static_cast<const __nv_bfloat16 *>(k), static_cast<const __nv_bfloat16 *>(v),
+                                         pp.kc, pp.vc, cu, cache->table, cache->lens, nseq, Hkv, cache->max_pages,
+                                         cache->n_pages, cache->page, pp.page_shift, status};
+            const long long blocks = (T * Hkv * (la::D / 8) + la::APPEND_THREADS - 1) / la::APPEND_THREADS;
+            if (!launch_dependent(la::la_cache_append_kernel, dim3((unsigned)(blocks < 148 * 8 ? blocks : 148 * 8)),
+                                  la::APPEND_THREADS, 0, stream, at, (int)T, static_cast<const int *>(sp.hdr)))
+                return LA_ERR_CUDA;
+            ++g_launches;
+        }
+    } else {
+        mkc = mk;
+        mvc = mv;
     }
     pp.out = static_cast<__nv_bfloat16 *>(out);
     pp.lse = lse;
@@ -204,39 +251,69 @@ la_status softmax_prefill_impl(const void *q, const void *k, const void *v, cons
     pp.scale_log2 = scale * kLog2e;
     pp.wait_limit_ns = g_wait_limit_ns.load();
     pp.status = status;
-    const int grid = (int)(items < device_sm_count() ? items : device_sm_count());
+    pp.direct = direct;
+    pp.cu = cu;
+    pp.nseq = nseq;
+    pp.T = (int)T;
+    pp.max_seqlen = max_seqlen;
+    pp.max_keys = max_keys;
     st = ensure_smem_attr(g_attr_softmax, la::la_softmax_prefill_kernel, la::SMX_SMEM);
     if (st != LA_OK) return st;
-    la::la_softmax_prefill_kernel<<<grid, la::SMX_THREADS, la::SMX_SMEM, stream>>>(mq, mk, mv, pp);
+    if (direct)
+        la::la_softmax_prefill_kernel<<<(unsigned)items, la::SMX_THREADS, la::SMX_SMEM, stream>>>(mq, mk, mv, mkc, mvc, pp);
+    else if (!launch_dependent(la::la_softmax_prefill_kernel, dim3((unsigned)sms), la::SMX_THREADS, la::SMX_SMEM, stream,
+                               mq, mk, mv, mkc, mvc, pp))
+        return LA_ERR_CUDA;
     if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
     ++g_launches;
     return LA_OK;
 }
 
-// Launch a kernel that may be set up while the one before it in the stream
-// still runs (it waits for that one's end itself, with griddepcontrol.wait).
-template <class... P, class... A>
-bool launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
-}
-
 constexpr size_t kDecodeParts = (size_t)la::SD_CTAS * 2 * la::SD_PART * sizeof(float);
 constexpr size_t kDecodeWs = kDecodeParts + (size_t)la::SD_CTAS * sizeof(int4);
+
+// CTAs of the cluster that a row of a decode step takes, 0 for the form that
+// cuts all rows' tiles into equal runs and joins them with a second kernel.  A
+// cluster per row needs few rows (all CTAs resident at once) and rows that are
+// not long, since only rows x cluster CTAs read, whatever the other rows'
+// lengths.  64 heads over 8, cluster / runs, in us: 1 request of 700 keys 7.2 /
+// 12.3, of 3000 9.8 / 20.4, of 16000 24.6 (cluster of 16: 19.5) / 28.1; 4 requests of
+// 700 keys 8.7 / 13.6, of 16000 44 / 53.  Clusters of 16 only while one wave of
+// them fits (2 requests of 700 keys: 13.8 against 7.7 in clusters of 8) and for
+// rows whose reading outweighs their longer meeting (1 request of 64 keys: 7.7
+// against 6.7).
+int decode_cluster(long long B, int H, int Hkv, long long max_keys) {
+    const int G = H / Hkv, chunks = (G + la::SD_HEADS - 1) / la::SD_HEADS;
+    const long long rows = B * Hkv * chunks;
+    if (max_keys > 16384 || rows * 8 > la::SD_CTAS) return 0;
+    return rows * 16 <= 148 && max_keys > 2048 ? 16 : 8;
+}
+
+template <int CLUSTER>
+la_status launch_decode_cluster(SmemAttr &attr, const CUtensorMap &mk, const CUtensorMap &mv,
+                                const la::SoftmaxDecodeParams &dp, cudaStream_t stream) {
+    auto kernel = la::la_softmax_decode_cluster_kernel<CLUSTER>;
+    la_status st = ensure_smem_attr(attr, kernel, la::SD_SMEM, CLUSTER > 8);
+    if (st != LA_OK) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)dp.B * dp.Hkv * dp.chunks * CLUSTER));
+    cfg.blockDim = dim3(la::SD_THREADS);
+    cfg.dynamicSmemBytes = la::SD_SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attrs = {};
+    attrs.id = cudaLaunchAttributeClusterDimension;
+    attrs.val.clusterDim.x = CLUSTER;
+    attrs.val.clusterDim.y = attrs.val.clusterDim.z = 1;
+    cfg.attrs = &attrs;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, mk, mv, dp) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
 
 }  // namespace
 
 size_t la_softmax_prefill_varlen_workspace_size(int nseq, int total_tokens, int H, int Hkv, int d) {
     if (nseq < 0 || total_tokens < 0 || check_softmax(H, Hkv, d, 1.f) != LA_OK) return 0;
-    return softmax_layout(nseq, total_tokens).total;
+    return softmax_items(nseq, total_tokens, H, Hkv).direct ? 0 : softmax_layout(nseq, total_tokens).total;
 }
 
 la_status la_softmax_prefill_varlen(const void *q, const void *k, const void *v, const int *cu_seqlens, int nseq,
@@ -260,9 +337,9 @@ la_status la_softmax_prefill_paged(const void *q, const void *k, const void *v, 
                                 lse, workspace, ws_bytes, stream);
 }
 
-size_t la_softmax_decode_paged_workspace_size(int B, int H, int Hkv, int d) {
-    if (B < 0 || check_softmax(H, Hkv, d, 1.f) != LA_OK) return 0;
-    return kDecodeWs;
+size_t la_softmax_decode_paged_workspace_size(int B, int H, int Hkv, int d, int page_size, int max_pages) {
+    if (B <= 0 || check_softmax(H, Hkv, d, 1.f) != LA_OK || page_size <= 0 || max_pages <= 0) return 0;
+    return decode_cluster(B, H, Hkv, (long long)page_size * max_pages) ? 0 : kDecodeWs;
 }
 
 la_status la_softmax_decode_paged(const void *q, const void *k, const void *v, int B, int H, int Hkv, int d,
@@ -289,11 +366,14 @@ la_status la_softmax_decode_paged(const void *q, const void *k, const void *v, i
         !clear_of(cache.k, in.n_cache, {q, k, v, n_q, n_kv, nullptr, 0}) ||
         !clear_of(cache.v, in.n_cache, {q, k, v, n_q, n_kv, nullptr, 0}))
         return LA_ERR_INVALID_ARGUMENT;
-    if (!workspace || ws_bytes < kDecodeWs) return LA_ERR_WORKSPACE;
-    if (!aligned(workspace, 256)) return LA_ERR_INVALID_ARGUMENT;
-    if (!clear_of(workspace, kDecodeWs, in) || ranges_overlap(workspace, kDecodeWs, out, n_out) ||
-        ranges_overlap(workspace, kDecodeWs, lse, n_lse))
-        return LA_ERR_INVALID_ARGUMENT;
+    const int cluster = decode_cluster(B, H, Hkv, (long long)max_pages * page_size);
+    if (!cluster) {
+        if (!workspace || ws_bytes < kDecodeWs) return LA_ERR_WORKSPACE;
+        if (!aligned(workspace, 256)) return LA_ERR_INVALID_ARGUMENT;
+        if (!clear_of(workspace, kDecodeWs, in) || ranges_overlap(workspace, kDecodeWs, out, n_out) ||
+            ranges_overlap(workspace, kDecodeWs, lse, n_lse))
+            return LA_ERR_INVALID_ARGUMENT;
+    }
     int *status = status_word();
     if (!status) return LA_ERR_CUDA;
     const long long cache_rows = (long long)n_pages * Hkv * page_size;
@@ -327,13 +407,20 @@ la_status la_softmax_decode_paged(const void *q, const void *k, const void *v, i
     dp.scale_log2 = scale * kLog2e;
     dp.wait_limit_ns = g_wait_limit_ns.load();
     dp.status = status;
+    if (cluster) {
+        st = cluster == 16 ? launch_decode_cluster<16>(g_attr_softmax_cluster16, mk, mv, dp, stream)
+                           : launch_decode_cluster<8>(g_attr_softmax_cluster, mk, mv, dp, stream);
+        if (st != LA_OK) return st;
+        ++g_launches;
+        return LA_OK;
+    }
     st = ensure_smem_attr(g_attr_softmax_decode, la::la_softmax_decode_kernel, la::SD_SMEM);
     if (st != LA_OK) return st;
     la::la_softmax_decode_kernel<<<la::SD_CTAS, la::SD_THREADS, la::SD_SMEM, stream>>>(mk, mv, dp);
     if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
     ++g_launches;
     if (!launch_dependent(la::la_softmax_join_kernel, dim3(la::SD_CTAS, dp.G < la::SD_HEADS ? dp.G : la::SD_HEADS),
-                          la::D, stream, dp))
+                          la::D, 0, stream, dp))
         return LA_ERR_CUDA;
     ++g_launches;
     return LA_OK;

@@ -46,9 +46,10 @@ def test_decode_matches_plain_attention(heads, page):
     decode([0, 1, 15, 16, 62, 63, 64, 65, 127, 128, 500], *heads, page=page, seed=heads[0] + page)
 
 
-@pytest.mark.parametrize("past", [[0], [5000], [3], [-1, 200, -1], [-1]], ids=str)
-def test_decode_few_requests(past):
-    decode(past, 16, 2, 32, seed=3 + len(past))
+@pytest.mark.parametrize("heads", [(16, 2), (64, 8), (40, 1)], ids=str)
+@pytest.mark.parametrize("past", [[0], [5000], [17000], [3], [-1, 200, -1], [-1], [900, 17]], ids=str)
+def test_decode_few_requests(past, heads):
+    decode(past, *heads, 32, seed=3 + len(past))
 
 
 def test_decode_fp32_output_and_scale():
@@ -64,7 +65,7 @@ def test_decode_many_requests():
 def test_decode_repeats_bit_for_bit_and_in_a_graph():
     """Replays of a captured step with lengths advanced on the device, two
     graphs sharing one workspace, against the same steps run eagerly."""
-    past, H, Hkv, page, steps = [200, 0, 63, 1000], 16, 2, 32, 6
+    past, H, Hkv, page, steps = [200, 0, 63, 1000], 160, 40, 32, 6  # too many rows for a cluster each
     B = len(past)
     ca, cb = (Cache(past, [steps] * B, Hkv, page, 21) for _ in range(2))
     q, k, v, _, _ = packed([steps * B], H, Hkv, 22)
@@ -74,7 +75,7 @@ def test_decode_repeats_bit_for_bit_and_in_a_graph():
         want.append(la.softmax_decode_paged(q[a].clone(), k[a].clone(), v[a].clone(), ca.k, ca.v, ca.table, ca.lens)[0])
         ca.lens += 1
     qs, ks, vs = q[:B].clone(), k[:B].clone(), v[:B].clone()
-    ws = torch.empty(la.lib().la_softmax_decode_paged_workspace_size(B, H, Hkv, 128), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(la.lib().la_softmax_decode_paged_workspace_size(B, H, Hkv, 128, page, cb.table.shape[1]), dtype=torch.uint8, device="cuda")
     outs = [torch.zeros_like(qs) for _ in range(2)]
     graphs = []
     for o in outs:
@@ -92,8 +93,9 @@ def test_decode_repeats_bit_for_bit_and_in_a_graph():
     assert torch.equal(ca.k.view(torch.int16), cb.k.view(torch.int16))
 
 
-def test_decode_bad_pages_and_lengths():
-    past, H, Hkv, page = [40, 40, 40, 40], 8, 2, 16
+@pytest.mark.parametrize("H,Hkv", [(8, 2), (16, 4), (16, 16)])
+def test_decode_bad_pages_and_lengths(H, Hkv):
+    past, page = [40, 40, 40, 40], 16
     c = Cache(past, [1] * 4, Hkv, page, 31)
     q, k, v, _, _ = packed([4], H, Hkv, 32)
     want, _ = la.softmax_decode_paged(q, k, v, c.k, c.v, c.table, c.lens)
