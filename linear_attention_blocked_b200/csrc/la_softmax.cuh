@@ -141,6 +141,26 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// ---- pairs of fp32 values in one 64-bit register (packed fp32 instructions) ----
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 // Bounded waits of a control block with `abort`: as wait_or_abort above.
 template <class Ctrl>
 __device__ __forceinline__ bool ctrl_wait(uint64_t *bar, uint32_t parity, unsigned long long limit_ns, int *status,
@@ -590,7 +610,8 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
                 }
                 float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < 128; ++i) mt[i & 3] = fmaxf(mt[i & 3], __uint_as_float(x[i]));
+                for (int i = 0; i < 128; i += 2)  // (three-input maxima)
+                    mt[(i >> 1) & 3] = fmaxf(mt[(i >> 1) & 3], fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
                 const float tile_max = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
                 if (j == 0) {
                     m = tile_max;
@@ -611,22 +632,26 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
                         }
                     }
                 }
-                const float mc = m * c;
-                float s4[4] = {0.f, 0.f, 0.f, 0.f};
+                const f32x2 c2 = pack2(c, c), mc2 = pack2(-m * c, -m * c);
+                f32x2 s2[2] = {0ull, 0ull};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {  // 32 columns at a time: 16 TMEM columns of bf16 pairs
                     uint32_t b[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float e0 = ex2(fmaf(__uint_as_float(x[q * 32 + 2 * i]), c, -mc));
-                        const float e1 = ex2(fmaf(__uint_as_float(x[q * 32 + 2 * i + 1]), c, -mc));
-                        s4[(2 * i) & 3] += e0;
-                        s4[(2 * i + 1) & 3] += e1;
+                        const int k = q * 32 + 2 * i;
+                        float e0, e1;
+                        unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, mc2), e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                        s2[i & 1] = add2(s2[i & 1], pack2(e0, e1));
                         b[i] = pack_bf16x2(e0, e1);  // one rounding to bf16, for the tensor cores
                     }
                     tmem_st16(ts + q * 16, b);
                 }
-                l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                float sa, sb;
+                unpack2(add2(s2[0], s2[1]), sa, sb);
+                l += sa + sb;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();

@@ -466,9 +466,14 @@ SoftmaxBwdLayout softmax_bwd_layout(int nseq, long long T, int H, int Hkv) {
     w.delta = w.lse2 + rows;
     w.parts = w.delta + rows;
     const int G = H / Hkv;
-    const long long items = w.tables.emax * Hkv, want = 8 * 148;
+    // The longest walk of dk and dv, over all of a sequence's rows for all of a
+    // group's heads, should be short against an SM's share of the whole: with one
+    // sequence it is 169 / items of that share.  (With many items one part is
+    // faster, 2.32 against 2.38 ms with two at 16908 tokens of 32 heads over 4:
+    // dq fills the SMs that run out, and no sums go through memory.)
+    const long long items = w.tables.emax * Hkv;
     w.nparts = 1;
-    while (w.nparts < 4 && 2 * w.nparts <= G && items * w.nparts < want) w.nparts *= 2;
+    while (2 * w.nparts <= G && items * w.nparts < 2 * 148) w.nparts *= 2;
     w.total = w.parts + (w.nparts > 1 ? (size_t)w.nparts * 2 * T * Hkv * la::D * sizeof(float) : 0);
     return w;
 }
@@ -560,19 +565,23 @@ la_status la_softmax_prefill_backward_varlen(const void *q, const void *k, const
         !encode_qkv_map(&mv, v, (int)T, Hkv) || !encode_qkv_map(&mg, dout, (int)T, H))
         return LA_ERR_CUDA;
     const long long row_blocks = (T * H + la::SB_ROWS_THREADS / 16 - 1) / (la::SB_ROWS_THREADS / 16);
-    la::la_softmax_rows_kernel<<<(unsigned)(row_blocks < 148 * 16 ? row_blocks : 148 * 16), la::SB_ROWS_THREADS, 0,
-                                 stream>>>(static_cast<const __nv_bfloat16 *>(out),
-                                           static_cast<const __nv_bfloat16 *>(dout), lse, lse2, delta, (int)T, H);
-    if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
+    if (!launch_dependent(la::la_softmax_rows_kernel, dim3((unsigned)(row_blocks < 148 * 16 ? row_blocks : 148 * 16)),
+                          la::SB_ROWS_THREADS, 0, stream, static_cast<const __nv_bfloat16 *>(out),
+                          static_cast<const __nv_bfloat16 *>(dout), lse, lse2, delta, (int)T, H))
+        return LA_ERR_CUDA;
     ++g_launches;
 
     if ((st = ensure_smem_attr(g_attr_softmax_dkv, la::la_softmax_dkv_kernel, la::DKV_SMEM)) != LA_OK) return st;
     if ((st = ensure_smem_attr(g_attr_softmax_dq, la::la_softmax_dq_kernel, la::DQ_SMEM)) != LA_OK) return st;
     const int sms = device_sm_count();
     const long long dkv_items = w.tables.emax * Hkv * (long long)w.nparts, dq_items = w.tables.emax * H;
-    la::la_softmax_dkv_kernel<<<(unsigned)(dkv_items < sms ? dkv_items : sms), la::SB_THREADS, la::DKV_SMEM, stream>>>(
-        mq, mk, mv, mg, bp);
-    if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
+    if (!launch_dependent(la::la_softmax_dkv_kernel, dim3((unsigned)(dkv_items < sms ? dkv_items : sms)), la::SB_THREADS,
+                          la::DKV_SMEM, stream, mq, mk, mv, mg, bp))
+        return LA_ERR_CUDA;
+    ++g_launches;
+    if (!launch_dependent(la::la_softmax_dq_kernel, dim3((unsigned)(dq_items < sms ? dq_items : sms)), la::SB_THREADS,
+                          la::DQ_SMEM, stream, mq, mk, mv, mg, bp))
+        return LA_ERR_CUDA;
     ++g_launches;
     if (w.nparts > 1) {
         const long long n = T * Hkv * la::D, blocks = (n / 2 + 255) / 256;
@@ -581,9 +590,5 @@ la_status la_softmax_prefill_backward_varlen(const void *q, const void *k, const
         if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
         ++g_launches;
     }
-    la::la_softmax_dq_kernel<<<(unsigned)(dq_items < sms ? dq_items : sms), la::SB_THREADS, la::DQ_SMEM, stream>>>(
-        mq, mk, mv, mg, bp);
-    if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
-    ++g_launches;
     return LA_OK;
 }

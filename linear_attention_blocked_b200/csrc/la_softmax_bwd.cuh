@@ -69,6 +69,7 @@ constexpr int SB_ROWS_THREADS = 256;
 __global__ void __launch_bounds__(SB_ROWS_THREADS)
 la_softmax_rows_kernel(const __nv_bfloat16 *out, const __nv_bfloat16 *dout, const float *lse, float *lse2,
                        float *delta, int T, int H) {
+    pdl_launch();  // (the kernel behind waits for this one's end before it reads the rows)
     const long long total = (long long)T * H;
     const int l16 = threadIdx.x & 15;
     for (long long e = ((long long)blockIdx.x * SB_ROWS_THREADS + threadIdx.x) >> 4; e < total;
@@ -90,6 +91,7 @@ la_softmax_rows_kernel(const __nv_bfloat16 *out, const __nv_bfloat16 *dout, cons
             lse2[h * T + t] = lse[e] * 1.44269504088896341f;
         }
     }
+    pdl_wait();  // the scheduler has ended when this kernel has
 }
 
 // ---------------------------------------------------------------------------
@@ -207,6 +209,8 @@ la_softmax_dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_cons
         if (warp == 0) {
             // ===================== items, Q and g tiles =====================
             const uint64_t pol = policy_evict_last();
+            pdl_wait();    // the tables and rows
+            pdl_launch();  // dq, which needs nothing of this kernel, fills the SMs that run out of items
             const int ne = p.hdr[HDR_G];
             const long long total = (long long)ne * p.Hkv * p.nparts;
             uint32_t it = 0, n = 0;
@@ -352,6 +356,7 @@ la_softmax_dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_cons
             // ===================== rows of the steps =====================
             // A query row behind the sequence's end: lse2 = +inf makes its P zero, and
             // its Q and g rows (another sequence's) are zeroed.
+            pdl_wait();
             uint32_t it = 0, n = 0;
             int im[BI_FIELDS];
             bool ok = true;
@@ -781,6 +786,9 @@ la_softmax_dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 512);
+    // This kernel may have started beside the one of dk and dv, which had seen the
+    // tables and rows complete; it ends no earlier.
+    pdl_wait();
 }
 
 }  // namespace la

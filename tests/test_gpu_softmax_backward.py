@@ -132,3 +132,10 @@ def test_bad_tables_and_calls_are_refused():
         la.softmax_prefill_backward_varlen(q, k, v, out, lse, g, cu_dev, 100, dq=g)
     with pytest.raises(TypeError):
         la.softmax_prefill_backward_varlen(q, k, v, out.float(), lse, g, cu_dev, 100)
+
+
+def test_gradients_of_a_shared_head_in_parts():
+    """One key/value head for many query heads: its key blocks' sums are formed
+    in parts by several CTAs."""
+    run_and_check([300, 1, 129], 24, 1, seed=29)
+    run_and_check([1300], 64, 1, seed=31)
