@@ -23,6 +23,13 @@ ABI (include/lightning_attn.h).  Entry points:
   prefill_backward_varlen(q, k, v, dout, cu, ...)  la_prefill_backward_varlen: the same per packed sequence
   prefill_from_host(q, k, v, ...)            la_prefill of pinned host tensors, chunks pipelined
                                              over copy-in / scan / copy-out streams
+  softmax_prefill_varlen(q, k, v, cu, ...)   la_softmax_prefill_varlen: causal softmax attention of
+                                             packed prompts, grouped key/value heads (the layers
+                                             between the Lightning layers of the hybrid model)
+  softmax_prefill_backward_varlen(...)       la_softmax_prefill_backward_varlen: dq, dk, dv
+  softmax_prefill_paged(q, k, v, cu, ...)    la_softmax_prefill_paged: prompt chunks on a paged cache
+  softmax_decode_paged(q, k, v, ...)         la_softmax_decode_paged: one new token per request
+  cache_copy_pages(k_cache, v_cache, ...)    la_cache_copy_pages (page numbers: serving.PagePool)
   get_device_status()                        la_get_device_status
 """
 from ._binding import (D, DEFAULT_BLOCK, backward_workspace_size, backward_varlen_workspace_size,  # noqa: F401
@@ -37,7 +44,7 @@ from ._binding import (D, DEFAULT_BLOCK, backward_workspace_size, backward_varle
 from .seqpar import (lasp_prefill, lasp_prefill_backward, lasp_prefill_backward_varlen,  # noqa: F401,E402
                      lasp_prefill_varlen, plan_varlen_rank,
                      split_tokens)
-from .serving import BatchPlan, plan_batch  # noqa: F401,E402
+from .serving import BatchPlan, PagePool, PoolExhausted, plan_batch  # noqa: F401,E402
 from .streaming import make_buffers, prefill_from_host  # noqa: F401,E402
 from .softmax import (cache_copy_pages, softmax_decode_paged, softmax_prefill_backward_varlen,  # noqa: F401,E402
                       softmax_prefill_paged, softmax_prefill_varlen)
