@@ -5,22 +5,51 @@ A call runs on the device of `q` and on `stream` (default: that device's
 current stream); what it allocates -- outputs that were not passed, and the
 workspace -- belongs to that stream.
 
-A decode step of one request takes some ten microseconds on the GPU, so the
-marshalling is kept short: one comparison per tensor and the reasons spelled
-out only when it fails, addresses as plain integers, workspace sizes (pure
-functions of the shapes) remembered.
+A decode step of one request takes some seven microseconds on the GPU, so the
+marshalling is kept short.  Calls of the plain kind (no stream or workspace
+passed, everything on the current device and as documented) go through a small
+compiled module where it is built; the others, and those with something wrong,
+through the Python code here, which checks everything and says what is wrong.
 """
 from __future__ import annotations
 
 import functools
+import importlib.machinery
+import importlib.util
+import os
 
 import torch
 
+from . import _build
 from ._binding import D, LA_BF16, LA_FP32, LA_OK, LAError, _need, lib
 
 SCALE = D ** -0.5
 _BF16, _FP32, _INT32 = torch.bfloat16, torch.float32, torch.int32
 _raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _load_marshal():
+    path = _build.marshal_path()
+    if not os.path.exists(path) or not os.path.exists(_build.LIB_PATH):
+        return None
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+        loader.exec_module(module)
+        return module
+    except ImportError:
+        return None
+
+
+_marshal = False  # not looked for yet
+
+
+def _module():
+    """The compiled module, or None."""
+    global _marshal
+    if _marshal is False:
+        _marshal = _load_marshal()
+    return _marshal
 
 
 def _fits(t, name, dtype, shape, dev):
@@ -64,7 +93,10 @@ def _dims(q, k, v):
     return T, H, Hkv, d, dev
 
 
-def _sequences(cu_seqlens, dev):
+def _sequences(cu_seqlens, max_seqlen, dev):
+    """Number of sequences, with max_seqlen a length."""
+    if not 0 <= max_seqlen <= 0x7FFFFFFF:
+        raise ValueError("max_seqlen must be a length")
     if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must hold nseq + 1 entries")
     _fits(cu_seqlens, "cu_seqlens", _INT32, cu_seqlens.shape, dev)
@@ -125,16 +157,17 @@ def _done(status, where):
         raise LAError(status, where)
 
 
+def _short(result, where):
+    """What the compiled module returned: results, a status, or None."""
+    if result.__class__ is int:
+        raise LAError(result, where)
+    return result
+
+
 @_on_stream
-def softmax_prefill_varlen(q, k, v, cu_seqlens, max_seqlen: int, scale=None, out=None, lse=None,
-                           want_lse: bool = True, workspace=None, *, handle):
-    """la_softmax_prefill_varlen: causal softmax attention of packed bf16
-    q [T, H, d] over k, v [T, Hkv, d] (H a multiple of Hkv) with device int32
-    cu_seqlens.  scale: factor of the scores, d**-0.5 by default; stream: the
-    device's current one by default.  Returns (out [T, H, d] bf16, lse [T, H]
-    fp32 or None)."""
+def _softmax_prefill_varlen(q, k, v, cu_seqlens, max_seqlen, scale, out, lse, want_lse, workspace, *, handle):
     T, H, Hkv, d, dev = _dims(q, k, v)
-    nseq = _sequences(cu_seqlens, dev)
+    nseq = _sequences(cu_seqlens, max_seqlen, dev)
     out = _like(out, "out", q, dev)
     lse = _rows(lse, want_lse, q, T, H, dev)
     ws, at, nbytes = _scratch(workspace, _size("la_softmax_prefill_varlen_workspace_size", nseq, T, H, Hkv, d), q, dev)
@@ -146,16 +179,13 @@ def softmax_prefill_varlen(q, k, v, cu_seqlens, max_seqlen: int, scale=None, out
 
 
 @_on_stream
-def softmax_prefill_backward_varlen(q, k, v, out, lse, dout, cu_seqlens, max_seqlen: int, scale=None, dq=None, dk=None,
-                                    dv=None, workspace=None, *, handle):
-    """la_softmax_prefill_backward_varlen: gradients of softmax_prefill_varlen
-    for dL/dout; out and lse are what that call returned, scale what it was
-    given.  Returns (dq [T, H, d], dk, dv [T, Hkv, d]) in bf16."""
+def _softmax_prefill_backward_varlen(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, scale, dq, dk, dv, workspace, *,
+                                     handle):
     T, H, Hkv, d, dev = _dims(q, k, v)
     _fits(out, "out", _BF16, (T, H, d), dev)
     _fits(lse, "lse", _FP32, (T, H), dev)
     _fits(dout, "dout", _BF16, (T, H, d), dev)
-    nseq = _sequences(cu_seqlens, dev)
+    nseq = _sequences(cu_seqlens, max_seqlen, dev)
     dq, dk, dv = _like(dq, "dq", q, dev), _like(dk, "dk", k, dev), _like(dv, "dv", v, dev)
     ws, at, nbytes = _scratch(workspace,
                               _size("la_softmax_prefill_backward_varlen_workspace_size", nseq, T, H, Hkv, d), q, dev)
@@ -168,16 +198,10 @@ def softmax_prefill_backward_varlen(q, k, v, out, lse, dout, cu_seqlens, max_seq
 
 
 @_on_stream
-def softmax_prefill_paged(q, k, v, cu_seqlens, max_seqlen: int, k_cache, v_cache, page_table, cache_lens, scale=None,
-                          out=None, lse=None, want_lse: bool = True, workspace=None, *, handle):
-    """la_softmax_prefill_paged: the packed new tokens q [T, H, d], k, v
-    [T, Hkv, d] of each sequence are written behind its cache_lens[i] cached
-    ones and attend to all of them, causally among themselves.  k_cache,
-    v_cache: bf16 [n_pages, Hkv, page_size, d], updated in place; page_table:
-    device int32 [nseq, max_pages]; cache_lens: device int32 [nseq], lengths
-    before the call.  Returns (out, lse or None)."""
+def _softmax_prefill_paged(q, k, v, cu_seqlens, max_seqlen, k_cache, v_cache, page_table, cache_lens, scale, out, lse,
+                           want_lse, workspace, *, handle):
     T, H, Hkv, d, dev = _dims(q, k, v)
-    nseq = _sequences(cu_seqlens, dev)
+    nseq = _sequences(cu_seqlens, max_seqlen, dev)
     n_pages, page, max_pages = _cache(k_cache, v_cache, page_table, cache_lens, nseq, Hkv, d, dev)
     out = _like(out, "out", q, dev)
     lse = _rows(lse, want_lse, q, T, H, dev)
@@ -192,13 +216,8 @@ def softmax_prefill_paged(q, k, v, cu_seqlens, max_seqlen: int, k_cache, v_cache
 
 
 @_on_stream
-def softmax_decode_paged(q, k, v, k_cache, v_cache, page_table, cache_lens, scale=None, out=None,
-                         out_dtype=torch.bfloat16, lse=None, want_lse: bool = True, workspace=None, *, handle):
-    """la_softmax_decode_paged: one new token per request, q [B, H, d], k, v
-    [B, Hkv, d], written behind the cache_lens[b] cached ones (-1: no request,
-    the row's outputs are left as they are).  The cache as for
-    softmax_prefill_paged.  Returns (out [B, H, d] bf16 or fp32, lse [B, H] or
-    None)."""
+def _softmax_decode_paged(q, k, v, k_cache, v_cache, page_table, cache_lens, scale, out, out_dtype, lse, want_lse,
+                          workspace, *, handle):
     B, H, Hkv, d, dev = _dims(q, k, v)
     n_pages, page, max_pages = _cache(k_cache, v_cache, page_table, cache_lens, B, Hkv, d, dev)
     dtype = out_dtype if out is None else out.dtype
@@ -211,8 +230,8 @@ def softmax_decode_paged(q, k, v, k_cache, v_cache, page_table, cache_lens, scal
     else:
         _fits(out, "out", _FP32, (B, H, d), dev)
     lse = _rows(lse, want_lse, q, B, H, dev)
-    ws, at, nbytes = _scratch(workspace, _size("la_softmax_decode_paged_workspace_size", B, H, Hkv, d, page, max_pages), q,
-                              dev)
+    nbytes = _size("la_softmax_decode_paged_workspace_size", B, H, Hkv, d, page, max_pages)
+    ws, at, nbytes = _scratch(workspace, nbytes, q, dev)
     _done(lib().la_softmax_decode_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(), B, H, Hkv, d,
                                         SCALE if scale is None else scale, k_cache.data_ptr(), v_cache.data_ptr(),
                                         n_pages, page, page_table.data_ptr(), max_pages, cache_lens.data_ptr(),
@@ -223,9 +242,7 @@ def softmax_decode_paged(q, k, v, k_cache, v_cache, page_table, cache_lens, scal
 
 
 @_on_stream
-def cache_copy_pages(k_cache, v_cache, src, dst, *, handle):
-    """la_cache_copy_pages: page src[i] is copied to page dst[i] in both
-    tensors [n_pages, Hkv, page_size, d]; src, dst: device int32 [n]."""
+def _cache_copy_pages(k_cache, v_cache, src, dst, *, handle):
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [n_pages, Hkv, page_size, d]")
     dev = k_cache.get_device()
@@ -237,3 +254,80 @@ def cache_copy_pages(k_cache, v_cache, src, dst, *, handle):
     _fits(dst, "dst", _INT32, (n,), dev)
     _done(lib().la_cache_copy_pages(k_cache.data_ptr(), v_cache.data_ptr(), n_pages, page, Hkv, d, src.data_ptr(),
                                     dst.data_ptr(), n, handle), "la_cache_copy_pages")
+
+
+def softmax_prefill_varlen(q, k, v, cu_seqlens, max_seqlen: int, scale=None, out=None, lse=None, want_lse: bool = True,
+                           workspace=None, stream=None):
+    """la_softmax_prefill_varlen: causal softmax attention of packed bf16
+    q [T, H, d] over k, v [T, Hkv, d] (H a multiple of Hkv) with device int32
+    cu_seqlens.  scale: factor of the scores, d**-0.5 by default; stream: the
+    device's current one by default.  Returns (out [T, H, d] bf16, lse [T, H]
+    fp32 or None)."""
+    if stream is None and workspace is None and _module() is not None:
+        done = _short(_marshal.prefill_varlen(q, k, v, cu_seqlens, max_seqlen, SCALE if scale is None else scale, out,
+                                              lse, want_lse), "la_softmax_prefill_varlen")
+        if done is not None:
+            return done
+    return _softmax_prefill_varlen(q, k, v, cu_seqlens, max_seqlen, scale, out, lse, want_lse, workspace, stream=stream)
+
+
+def softmax_prefill_backward_varlen(q, k, v, out, lse, dout, cu_seqlens, max_seqlen: int, scale=None, dq=None, dk=None,
+                                    dv=None, workspace=None, stream=None):
+    """la_softmax_prefill_backward_varlen: gradients of softmax_prefill_varlen
+    for dL/dout; out and lse are what that call returned, scale what it was
+    given.  Returns (dq [T, H, d], dk, dv [T, Hkv, d]) in bf16."""
+    if stream is None and workspace is None and _module() is not None:
+        done = _short(_marshal.prefill_backward_varlen(q, k, v, out, lse, dout, cu_seqlens, max_seqlen,
+                                                       SCALE if scale is None else scale, dq, dk, dv),
+                      "la_softmax_prefill_backward_varlen")
+        if done is not None:
+            return done
+    return _softmax_prefill_backward_varlen(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, scale, dq, dk, dv,
+                                            workspace, stream=stream)
+
+
+def softmax_prefill_paged(q, k, v, cu_seqlens, max_seqlen: int, k_cache, v_cache, page_table, cache_lens, scale=None,
+                          out=None, lse=None, want_lse: bool = True, workspace=None, stream=None):
+    """la_softmax_prefill_paged: the packed new tokens q [T, H, d], k, v
+    [T, Hkv, d] of each sequence are written behind its cache_lens[i] cached
+    ones and attend to all of them, causally among themselves.  k_cache,
+    v_cache: bf16 [n_pages, Hkv, page_size, d], updated in place; page_table:
+    device int32 [nseq, max_pages]; cache_lens: device int32 [nseq], lengths
+    before the call.  Returns (out, lse or None)."""
+    if stream is None and workspace is None and _module() is not None:
+        done = _short(_marshal.prefill_paged(q, k, v, cu_seqlens, max_seqlen, k_cache, v_cache, page_table, cache_lens,
+                                             SCALE if scale is None else scale, out, lse, want_lse),
+                      "la_softmax_prefill_paged")
+        if done is not None:
+            return done
+    return _softmax_prefill_paged(q, k, v, cu_seqlens, max_seqlen, k_cache, v_cache, page_table, cache_lens, scale, out,
+                                  lse, want_lse, workspace, stream=stream)
+
+
+def softmax_decode_paged(q, k, v, k_cache, v_cache, page_table, cache_lens, scale=None, out=None,
+                         out_dtype=torch.bfloat16, lse=None, want_lse: bool = True, workspace=None, stream=None):
+    """la_softmax_decode_paged: one new token per request, q [B, H, d], k, v
+    [B, Hkv, d], written behind the cache_lens[b] cached ones (-1: no request,
+    the row's outputs are left as they are).  The cache as for
+    softmax_prefill_paged.  Returns (out [B, H, d] bf16 or fp32, lse [B, H] or
+    None)."""
+    if stream is None and workspace is None and _module() is not None:
+        dtype = out.dtype if isinstance(out, torch.Tensor) else out_dtype
+        if dtype is not _BF16 and dtype is not _FP32:
+            raise TypeError("out dtype must be torch.bfloat16 or torch.float32")
+        done = _short(_marshal.decode_paged(q, k, v, k_cache, v_cache, page_table, cache_lens,
+                                            SCALE if scale is None else scale, out, dtype is _FP32, lse, want_lse),
+                      "la_softmax_decode_paged")
+        if done is not None:
+            return done
+    return _softmax_decode_paged(q, k, v, k_cache, v_cache, page_table, cache_lens, scale, out, out_dtype, lse,
+                                 want_lse, workspace, stream=stream)
+
+
+def cache_copy_pages(k_cache, v_cache, src, dst, stream=None):
+    """la_cache_copy_pages: page src[i] is copied to page dst[i] in both
+    tensors [n_pages, Hkv, page_size, d]; src, dst: device int32 [n]."""
+    if stream is None and _module() is not None:
+        if _short(_marshal.copy_pages(k_cache, v_cache, src, dst), "la_cache_copy_pages") is not None:
+            return
+    _cache_copy_pages(k_cache, v_cache, src, dst, stream=stream)
