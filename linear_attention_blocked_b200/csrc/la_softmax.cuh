@@ -365,11 +365,12 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
             const uint64_t pol = policy_evict_last();
             int total = 0, ne = 0;
             int4 own = make_int4(0, 0, 0, 0);
+            pdl_wait();    // what came before has ended: inputs and, when not direct, tables
+            pdl_launch();  // the kernel behind may be set up (it waits for this one's end)
             if (p.direct) {
                 const int e = blockIdx.x / (p.Hkv * p.pairs);
                 total = e < smx_find(e, lane, p, own) ? 1 : 0;
             } else {
-                pdl_wait();  // the scheduler's tables
                 total = p.hdr[HDR_TOTAL];
                 ne = p.hdr[HDR_G];
             }
@@ -569,6 +570,7 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
             // ===================== new tokens into their pages =====================
             // (no CTA reads them there: their tiles come from the packed tensors)
             int4 unused;
+            pdl_wait();
             if (smx_find(-1, lane, p, unused) > 0) {
                 const AppendTables at = {p.new_k, p.new_v, p.kc, p.vc, p.cu, p.pages, p.past, p.nseq,
                                          p.Hkv, p.max_pages, p.n_pages, p.page, p.page_shift, p.status};
@@ -729,6 +731,7 @@ __global__ void __launch_bounds__(SCHED_THREADS, 1) la_softmax_schedule_kernel(c
     __shared__ int warp_sums[SCHED_THREADS / 32];
     __shared__ int carry_sh;
     const int tid = threadIdx.x;
+    pdl_wait();    // before the kernel behind may start: it reads what came before this one
     pdl_launch();
     int bad = 0;
     if (tid == 0 && (s.cu[0] != 0 || s.cu[s.nseq] != s.T)) bad = 1;

@@ -26,7 +26,7 @@ SoftmaxLayout softmax_layout(int nseq, long long T) {
 
 // Work items of the prompt kernel: pairs of query tiles.  With no more items
 // than SMs every CTA has one at most, which it finds itself: no scheduler launch
-// and no workspace (129 tokens, 64 heads over 8: 14.4 us with, 12.3 us without).
+// and no workspace (129 tokens, 64 heads over 8: 14.4 us with, 12.3 us without; back to back, with the next call set up meanwhile, 10.2 us).
 // Depends on the shape only, so that the workspace size does.
 struct SoftmaxItems {
     int rows, pairs;   // rows per entry, pairs per entry and key/value head
@@ -197,8 +197,7 @@ la_status softmax_prefill_impl(const void *q, const void *k, const void *v, cons
     sp.entries = reinterpret_cast<int4 *>(ws + w.entries);
     sp.status = status;
     if (!direct) {  // (without tokens only the tables are checked)
-        la::la_softmax_schedule_kernel<<<1, la::SCHED_THREADS, 0, stream>>>(sp);
-        if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
+        if (!launch_dependent(la::la_softmax_schedule_kernel, dim3(1), la::SCHED_THREADS, 0, stream, sp)) return LA_ERR_CUDA;
         ++g_launches;
         if (T == 0) return LA_OK;
     }
@@ -259,12 +258,9 @@ la_status softmax_prefill_impl(const void *q, const void *k, const void *v, cons
     pp.max_keys = max_keys;
     st = ensure_smem_attr(g_attr_softmax, la::la_softmax_prefill_kernel, la::SMX_SMEM);
     if (st != LA_OK) return st;
-    if (direct)
-        la::la_softmax_prefill_kernel<<<(unsigned)items, la::SMX_THREADS, la::SMX_SMEM, stream>>>(mq, mk, mv, mkc, mvc, pp);
-    else if (!launch_dependent(la::la_softmax_prefill_kernel, dim3((unsigned)sms), la::SMX_THREADS, la::SMX_SMEM, stream,
-                               mq, mk, mv, mkc, mvc, pp))
+    if (!launch_dependent(la::la_softmax_prefill_kernel, dim3((unsigned)(direct ? items : sms)), la::SMX_THREADS,
+                          la::SMX_SMEM, stream, mq, mk, mv, mkc, mvc, pp))
         return LA_ERR_CUDA;
-    if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
     ++g_launches;
     return LA_OK;
 }
@@ -300,12 +296,14 @@ la_status launch_decode_cluster(SmemAttr &attr, const CUtensorMap &mk, const CUt
     cfg.blockDim = dim3(la::SD_THREADS);
     cfg.dynamicSmemBytes = la::SD_SMEM;
     cfg.stream = stream;
-    cudaLaunchAttribute attrs = {};
-    attrs.id = cudaLaunchAttributeClusterDimension;
-    attrs.val.clusterDim.x = CLUSTER;
-    attrs.val.clusterDim.y = attrs.val.clusterDim.z = 1;
-    cfg.attrs = &attrs;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attrs[2] = {};
+    attrs[0].id = cudaLaunchAttributeClusterDimension;
+    attrs[0].val.clusterDim.x = CLUSTER;
+    attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, mk, mv, dp) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 
@@ -416,8 +414,8 @@ la_status la_softmax_decode_paged(const void *q, const void *k, const void *v, i
     }
     st = ensure_smem_attr(g_attr_softmax_decode, la::la_softmax_decode_kernel, la::SD_SMEM);
     if (st != LA_OK) return st;
-    la::la_softmax_decode_kernel<<<la::SD_CTAS, la::SD_THREADS, la::SD_SMEM, stream>>>(mk, mv, dp);
-    if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
+    if (!launch_dependent(la::la_softmax_decode_kernel, dim3(la::SD_CTAS), la::SD_THREADS, la::SD_SMEM, stream, mk, mv, dp))
+        return LA_ERR_CUDA;
     ++g_launches;
     if (!launch_dependent(la::la_softmax_join_kernel, dim3(la::SD_CTAS, dp.G < la::SD_HEADS ? dp.G : la::SD_HEADS),
                           la::D, 0, stream, dp))
@@ -440,10 +438,10 @@ la_status la_cache_copy_pages(void *k_cache, void *v_cache, int n_pages, int pag
     if (!status) return LA_ERR_CUDA;
     const long long pieces = (long long)((page_bytes + la::COPY_PIECE - 1) / la::COPY_PIECE);
     const long long blocks = 2 * pieces * n, most = 148 * 16;
-    la::la_cache_copy_kernel<<<(unsigned)(blocks < most ? blocks : most), la::COPY_THREADS, 0, stream>>>(
-        static_cast<uint8_t *>(k_cache), static_cast<uint8_t *>(v_cache), src, dst, n, n_pages, (long long)page_bytes,
-        status);
-    if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
+    if (!launch_dependent(la::la_cache_copy_kernel, dim3((unsigned)(blocks < most ? blocks : most)), la::COPY_THREADS, 0,
+                          stream, static_cast<uint8_t *>(k_cache), static_cast<uint8_t *>(v_cache), src, dst, n, n_pages,
+                          (long long)page_bytes, status))
+        return LA_ERR_CUDA;
     ++g_launches;
     return LA_OK;
 }
@@ -535,8 +533,7 @@ la_status la_softmax_prefill_backward_varlen(const void *q, const void *k, const
     sp.prefix = reinterpret_cast<int *>(ws + w.tables.prefix);
     sp.entries = reinterpret_cast<int4 *>(ws + w.tables.entries);
     sp.status = status;
-    la::la_softmax_schedule_kernel<<<1, la::SCHED_THREADS, 0, stream>>>(sp);
-    if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
+    if (!launch_dependent(la::la_softmax_schedule_kernel, dim3(1), la::SCHED_THREADS, 0, stream, sp)) return LA_ERR_CUDA;
     ++g_launches;
     if (T == 0) return LA_OK;
 

@@ -360,6 +360,7 @@ la_softmax_decode_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_c
     __shared__ DecodeCursor sh_start;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    pdl_wait();                      // the cache and lengths as the kernels before leave them
     pdl_launch();                    // the join kernel may be set up meanwhile (it waits for this one's end)
     if (smem_u32(smem) & 1023) {     // the swizzle's atoms
         if (tid == 0) {
@@ -502,6 +503,9 @@ la_softmax_decode_cluster_kernel(const __grid_constant__ CUtensorMap tmk, const 
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int rank = blockIdx.x % SD_CLUSTER, cl = blockIdx.x / SD_CLUSTER;
     const int R = p.Hkv * p.chunks, b = cl / R, crow = cl - b * R;
+    if (tid == 0) sd_init(&sh.cb);
+    pdl_wait();    // the cache and lengths as the kernels before leave them
+    pdl_launch();  // the kernel behind may be set up (it waits for this one's end)
     const int len = p.lens[b], nt = sd_tiles(len, p.max_keys);
     if (smem_u32(smem) & 1023) {  // (the same in every CTA)
         if (tid == 0) record_status(p.status, ST_CUDA);
@@ -511,7 +515,6 @@ la_softmax_decode_cluster_kernel(const __grid_constant__ CUtensorMap tmk, const 
         if (tid == 0 && crow == 0 && rank == 0 && len != -1) record_status(p.status, ST_INVALID);
         return;
     }
-    if (tid == 0) sd_init(&sh.cb);
     __syncthreads();
     const int tile0 = (int)((long long)nt * rank / SD_CLUSTER), tile1 = (int)((long long)nt * (rank + 1) / SD_CLUSTER);
     const float *red = reinterpret_cast<const float *>(smem + SD_RED);
@@ -608,6 +611,8 @@ constexpr int COPY_PIECE = COPY_THREADS * 64;
 __global__ void __launch_bounds__(COPY_THREADS) la_cache_copy_kernel(uint8_t *kc, uint8_t *vc, const int *src,
                                                                      const int *dst, int n, int n_pages,
                                                                      long long page_bytes, int *status) {
+    pdl_wait();
+    pdl_launch();
     const int pieces = (int)((page_bytes + COPY_PIECE - 1) / COPY_PIECE);
     const long long total = 2LL * n * pieces;
     for (long long e = blockIdx.x; e < total; e += gridDim.x) {
