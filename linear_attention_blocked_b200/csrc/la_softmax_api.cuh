@@ -5,7 +5,7 @@
 
 namespace {
 
-SmemAttr g_attr_softmax, g_attr_softmax_decode, g_attr_softmax_cluster, g_attr_softmax_cluster16, g_attr_softmax_dkv, g_attr_softmax_dq;
+SmemAttr g_attr_softmax, g_attr_softmax_dkv, g_attr_softmax_dq;
 
 struct SoftmaxLayout {
     size_t hdr, prefix, entries, total;
@@ -268,43 +268,86 @@ la_status softmax_prefill_impl(const void *q, const void *k, const void *v, cons
 constexpr size_t kDecodeParts = (size_t)la::SD_CTAS * 2 * la::SD_PART * sizeof(float);
 constexpr size_t kDecodeWs = kDecodeParts + (size_t)la::SD_CTAS * sizeof(int4);
 
-// CTAs of the cluster that a row of a decode step takes, 0 for the form that
-// cuts all rows' tiles into equal runs and joins them with a second kernel.  A
-// cluster per row needs few rows (all CTAs resident at once) and rows that are
-// not long, since only rows x cluster CTAs read, whatever the other rows'
-// lengths.  64 heads over 8, cluster / runs, in us: 1 request of 700 keys 7.2 /
-// 12.3, of 3000 9.8 / 20.4, of 16000 24.6 (cluster of 16: 19.5) / 28.1; 4 requests of
-// 700 keys 8.7 / 13.6, of 16000 44 / 53.  Clusters of 16 only while one wave of
-// them fits (2 requests of 700 keys: 13.8 against 7.7 in clusters of 8) and for
-// rows whose reading outweighs their longer meeting (1 request of 64 keys: 7.7
-// against 6.7).
+int decode_heads(int G) { return G > la::SD_NARROW ? la::SD_WIDE : la::SD_NARROW; }
+
+// CTAs (a cluster) that a row of a decode step takes, 0 for the form that cuts
+// all rows' tiles into equal runs and joins them with a second kernel.  CTAs per
+// row need no second kernel and leave their order to the hardware's scheduler,
+// but a row that is much longer than the others holds them up, and few rows do
+// not fill the GPU: so the largest cluster that keeps all CTAs resident, and rows
+// of at most some 2048 keys per CTA.  64 heads over 8, us, rows of the length given
+// (in brackets: of lengths up to it), in that form / in runs: 1 request of 64 keys
+// 5.7 / 8.3, of 4000 9.8 / 18.5, of 32000 (cluster of 16) 27.6 / 37.4; 4 of 16000 43
+// [29] / 49 [33]; 9 of 2000 15.4 [13.8] / 18.0 [13.9], of 8000 48 [38] / 53 [31]; 18 of
+// 1000 13.4 [11.8] / 18.7 [13.9], of 4000 47 [34] / 53 [30]; 32 of 4000 81 [48] / 87 [48];
+// 256 of 4000 582 [293] / 615 [316], of 8000 no difference.  Clusters of 16 only while
+// one wave of them fits (2 requests of 700 keys: 13.8 against 7.7 in clusters of 8)
+// and for rows whose reading outweighs their longer meeting (1 request of 16000 keys
+// 17.5 against 20.0 in a cluster of 8, of 64 keys 7.3 against 5.7).
 int decode_cluster(long long B, int H, int Hkv, long long max_keys) {
-    const int G = H / Hkv, chunks = (G + la::SD_HEADS - 1) / la::SD_HEADS;
+    const int G = H / Hkv, heads = decode_heads(G), chunks = (G + heads - 1) / heads;
     const long long rows = B * Hkv * chunks;
-    if (max_keys > 16384 || rows * 8 > la::SD_CTAS) return 0;
-    return rows * 16 <= 148 && max_keys > 2048 ? 16 : 8;
+    if (rows * 16 <= 148 && max_keys > 4096) return max_keys <= 32768 ? 16 : 0;
+    for (int c = 8; c > 1; c /= 2)
+        if (rows * c <= 256) return max_keys <= 2048 * c ? c : 0;
+    return max_keys <= (rows >= 256 ? 4096 : 2048) ? 1 : 0;
 }
 
-template <int CLUSTER>
-la_status launch_decode_cluster(SmemAttr &attr, const CUtensorMap &mk, const CUtensorMap &mv,
-                                const la::SoftmaxDecodeParams &dp, cudaStream_t stream) {
-    auto kernel = la::la_softmax_decode_cluster_kernel<CLUSTER>;
-    la_status st = ensure_smem_attr(attr, kernel, la::SD_SMEM, CLUSTER > 8);
+template <int HEADS, int STAGES, int CLUSTER>
+la_status launch_decode_cluster(const CUtensorMap &mk, const CUtensorMap &mv, const la::SoftmaxDecodeParams &dp,
+                                cudaStream_t stream) {
+    using S = la::DecodeShape<HEADS, STAGES>;
+    static SmemAttr attr;
+    auto kernel = la::la_softmax_decode_cluster_kernel<HEADS, STAGES, CLUSTER>;
+    la_status st = ensure_smem_attr(attr, kernel, S::SMEM, CLUSTER > 8);
     if (st != LA_OK) return st;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)dp.B * dp.Hkv * dp.chunks * CLUSTER));
-    cfg.blockDim = dim3(la::SD_THREADS);
-    cfg.dynamicSmemBytes = la::SD_SMEM;
+    cfg.blockDim = dim3(S::THREADS);
+    cfg.dynamicSmemBytes = S::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attrs[2] = {};
-    attrs[0].id = cudaLaunchAttributeClusterDimension;
-    attrs[0].val.clusterDim.x = CLUSTER;
-    attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
-    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[1].val.programmaticStreamSerializationAllowed = 1;
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = CLUSTER;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
     cfg.attrs = attrs;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = CLUSTER > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, mk, mv, dp) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
+
+template <int HEADS, int STAGES>
+la_status launch_decode_rows(int cluster, const CUtensorMap &mk, const CUtensorMap &mv,
+                             const la::SoftmaxDecodeParams &dp, cudaStream_t stream) {
+    switch (cluster) {
+    case 8: return launch_decode_cluster<HEADS, STAGES, 8>(mk, mv, dp, stream);
+    case 4: return launch_decode_cluster<HEADS, STAGES, 4>(mk, mv, dp, stream);
+    case 2: return launch_decode_cluster<HEADS, STAGES, 2>(mk, mv, dp, stream);
+    default: return launch_decode_cluster<HEADS, STAGES, 1>(mk, mv, dp, stream);
+    }
+}
+
+template <int HEADS>
+la_status launch_decode(int cluster, const CUtensorMap &mk, const CUtensorMap &mv, const la::SoftmaxDecodeParams &dp,
+                        cudaStream_t stream) {
+    if (cluster == 16) return launch_decode_cluster<HEADS, 3, 16>(mk, mv, dp, stream);
+    if (cluster) {
+        // The deep ring where CTAs have an SM each (clusters of them need room in one
+        // part of the GPU, so fewer) and more tiles than the short ring holds.  64 heads
+        // over 8, deep / short: 1 request of 4000 keys, one CTA a row, 31.5 / 36 us; of 16000,
+        // clusters of 8, 20.0 / 23; 2 of 3000 in clusters of 8 12.7 / 8.8; 1 of 700 7.2 / 6.3.
+        const long long ctas = (long long)dp.B * dp.Hkv * dp.chunks * cluster;
+        const bool deep = ctas <= (cluster == 1 ? 148 : 96) && dp.max_keys > 3 * la::SD_KEYS * cluster;
+        return deep ? launch_decode_rows<HEADS, 6>(cluster, mk, mv, dp, stream)
+                    : launch_decode_rows<HEADS, 3>(cluster, mk, mv, dp, stream);
+    }
+    using S = la::DecodeShape<HEADS, 3>;
+    static SmemAttr attr;
+    auto kernel = la::la_softmax_decode_kernel<HEADS>;
+    la_status st = ensure_smem_attr(attr, kernel, S::SMEM);
+    if (st != LA_OK) return st;
+    return launch_dependent(kernel, dim3(la::SD_CTAS), S::THREADS, S::SMEM, stream, mk, mv, dp) ? LA_OK : LA_ERR_CUDA;
 }
 
 }  // namespace
@@ -396,7 +439,7 @@ la_status la_softmax_decode_paged(const void *q, const void *k, const void *v, i
     dp.H = H;
     dp.Hkv = Hkv;
     dp.G = H / Hkv;
-    dp.chunks = (dp.G + la::SD_HEADS - 1) / la::SD_HEADS;
+    dp.chunks = (dp.G + decode_heads(dp.G) - 1) / decode_heads(dp.G);
     dp.max_pages = max_pages;
     dp.n_pages = n_pages;
     dp.page = page_size;
@@ -405,19 +448,12 @@ la_status la_softmax_decode_paged(const void *q, const void *k, const void *v, i
     dp.scale_log2 = scale * kLog2e;
     dp.wait_limit_ns = g_wait_limit_ns.load();
     dp.status = status;
-    if (cluster) {
-        st = cluster == 16 ? launch_decode_cluster<16>(g_attr_softmax_cluster16, mk, mv, dp, stream)
-                           : launch_decode_cluster<8>(g_attr_softmax_cluster, mk, mv, dp, stream);
-        if (st != LA_OK) return st;
-        ++g_launches;
-        return LA_OK;
-    }
-    st = ensure_smem_attr(g_attr_softmax_decode, la::la_softmax_decode_kernel, la::SD_SMEM);
+    st = decode_heads(dp.G) == la::SD_WIDE ? launch_decode<la::SD_WIDE>(cluster, mk, mv, dp, stream)
+                                           : launch_decode<la::SD_NARROW>(cluster, mk, mv, dp, stream);
     if (st != LA_OK) return st;
-    if (!launch_dependent(la::la_softmax_decode_kernel, dim3(la::SD_CTAS), la::SD_THREADS, la::SD_SMEM, stream, mk, mv, dp))
-        return LA_ERR_CUDA;
     ++g_launches;
-    if (!launch_dependent(la::la_softmax_join_kernel, dim3(la::SD_CTAS, dp.G < la::SD_HEADS ? dp.G : la::SD_HEADS),
+    if (cluster) return LA_OK;
+    if (!launch_dependent(la::la_softmax_join_kernel, dim3(la::SD_CTAS, dp.G < la::SD_WIDE ? dp.G : la::SD_WIDE),
                           la::D, 0, stream, dp))
         return LA_ERR_CUDA;
     ++g_launches;

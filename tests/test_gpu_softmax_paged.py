@@ -182,3 +182,14 @@ def test_copied_pages(page, Hkv):
     keep = [i for i in range(20) if i not in (2, 4, 5)]
     kc[dst[keep].long()] = kc[src[keep].long()]
     assert torch.equal(kc2, kc)
+
+
+@pytest.mark.parametrize("heads", [(8, 1), (16, 16), (24, 2)], ids=str)
+def test_decode_in_every_form(heads):
+    """The batch's size and the table's width choose between clusters per row and
+    runs of tiles: widths and batches on both sides of each border."""
+    for B, longest in [(1, 200), (1, 4500), (1, 33000), (2, 2100), (3, 9000), (5, 20000), (9, 3000), (17, 2500),
+                       (40, 1500), (130, 300), (260, 90)]:
+        past = [(longest * 7919 * (i + 1)) % (longest + 1) for i in range(B)]
+        past[-1] = longest
+        decode(past, *heads, page=128 if longest > 1000 else 32, seed=B)
