@@ -407,7 +407,7 @@ LA_API la_status la_prefill_backward_varlen(const void *q, const void *k, const 
  *   q            device bf16 [total_tokens, H, d];  k, v: [total_tokens, Hkv, d],
  *                H a multiple of Hkv.
  *   cu_seqlens, nseq, max_seqlen   as for la_prefill_varlen.
- *   scale        a positive finite factor of the scores (usually d^-0.5).
+ *   scale        a positive factor of the scores, at most 1e38 (usually d^-0.5).
  *   out          device bf16 [total_tokens, H, d].
  *   lse          device fp32 [total_tokens, H], or NULL.  The backward pass
  *                needs it; with it partial results over disjoint keys can be
@@ -440,7 +440,10 @@ LA_API la_status la_softmax_prefill_varlen(const void *q, const void *k, const v
  * dq: bf16 [total_tokens, H, d]; dk, dv: bf16 [total_tokens, Hkv, d]; the four
  * and the workspace (la_softmax_prefill_backward_varlen_workspace_size bytes,
  * 256-byte aligned) must not overlap the inputs or each other.  The gradient of
- * lse is not taken.  Otherwise as la_softmax_prefill_varlen. */
+ * lse is not taken.  P and dS are rounded to bf16 once each for the products
+ * that sum over them.  A value of dout that is not finite may reach dv of later
+ * rows of the same sequence in the same 128 rows.  Otherwise as
+ * la_softmax_prefill_varlen. */
 LA_API size_t la_softmax_prefill_backward_varlen_workspace_size(int nseq, int total_tokens, int H,
                                                                 int Hkv, int d);
 

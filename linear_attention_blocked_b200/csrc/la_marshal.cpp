@@ -104,6 +104,13 @@ bool number(PyObject *o, int &x) {
     return true;
 }
 
+// 1 or 0; -1 for what has no truth value
+int truth(PyObject *o) {
+    const int x = PyObject_IsTrue(o);
+    if (x < 0) PyErr_Clear();
+    return x;
+}
+
 PyObject *result(la_status st, const at::Tensor &out, const at::Tensor &lse) {
     if (st != LA_OK) return PyLong_FromLong(st);
     PyObject *a = THPVariable_Wrap(out);
@@ -134,7 +141,9 @@ PyObject *prefill_varlen(PyObject *, PyObject *const *a, Py_ssize_t n) {
             Py_RETURN_NONE;
         at::Tensor out, lse, ws;
         if (!output(a[6], out, {x.T, x.H, x.d}, BF16, x.dev)) Py_RETURN_NONE;
-        if ((a[7] != Py_None || PyObject_IsTrue(a[8]) == 1) && !output(a[7], lse, {x.T, x.H}, FP32, x.dev)) Py_RETURN_NONE;
+        const int want = truth(a[8]);
+        if (want < 0) Py_RETURN_NONE;
+        if ((a[7] != Py_None || want) && !output(a[7], lse, {x.T, x.H}, FP32, x.dev)) Py_RETURN_NONE;
         const int nseq = (int)cu.size(0) - 1;
         const size_t bytes = la_softmax_prefill_varlen_workspace_size(nseq, x.T, x.H, x.Hkv, x.d);
         if (bytes) ws = make({(int64_t)bytes}, at::kByte, x.dev);
@@ -159,7 +168,9 @@ PyObject *prefill_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
             Py_RETURN_NONE;
         at::Tensor out, lse, ws;
         if (!output(a[10], out, {x.T, x.H, x.d}, BF16, x.dev)) Py_RETURN_NONE;
-        if ((a[11] != Py_None || PyObject_IsTrue(a[12]) == 1) && !output(a[11], lse, {x.T, x.H}, FP32, x.dev)) Py_RETURN_NONE;
+        const int want = truth(a[12]);
+        if (want < 0) Py_RETURN_NONE;
+        if ((a[11] != Py_None || want) && !output(a[11], lse, {x.T, x.H}, FP32, x.dev)) Py_RETURN_NONE;
         const int nseq = (int)cu.size(0) - 1;
         const size_t bytes = la_softmax_prefill_paged_workspace_size(nseq, x.T, x.H, x.Hkv, x.d);
         if (bytes) ws = make({(int64_t)bytes}, at::kByte, x.dev);
@@ -182,7 +193,9 @@ PyObject *decode_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
         at::Tensor out, lse, ws;
         const auto type = a[9] == Py_True ? FP32 : BF16;
         if (!output(a[8], out, {x.T, x.H, x.d}, type, x.dev)) Py_RETURN_NONE;
-        if ((a[10] != Py_None || PyObject_IsTrue(a[11]) == 1) && !output(a[10], lse, {x.T, x.H}, FP32, x.dev)) Py_RETURN_NONE;
+        const int want = truth(a[11]);
+        if (want < 0) Py_RETURN_NONE;
+        if ((a[10] != Py_None || want) && !output(a[10], lse, {x.T, x.H}, FP32, x.dev)) Py_RETURN_NONE;
         const size_t bytes = la_softmax_decode_paged_workspace_size(x.T, x.H, x.Hkv, x.d, c.page, c.max_pages);
         if (bytes) ws = make({(int64_t)bytes}, at::kByte, x.dev);
         const la_status st = la_softmax_decode_paged(

@@ -46,7 +46,7 @@ SoftmaxItems softmax_items(int nseq, long long T, int H, int Hkv) {
 
 la_status check_softmax(int H, int Hkv, int d, float scale) {
     if (H <= 0 || Hkv <= 0 || d <= 0 || H % Hkv) return LA_ERR_INVALID_ARGUMENT;
-    if (!(scale > 0.f) || scale > 3.0e38f) return LA_ERR_INVALID_ARGUMENT;  // also rejects NaN
+    if (!(scale > 0.f) || scale > 1.0e38f) return LA_ERR_INVALID_ARGUMENT;  // also rejects NaN
     if (d != la::D) return LA_ERR_UNSUPPORTED;
     return LA_OK;
 }

@@ -25,8 +25,10 @@ def everything():
     c = Cache([20, 0, 100], [150, 1, 30], 2, 16, 4)
     got += la.softmax_prefill_paged(q, k, v, cu_dev, 150, c.k, c.v, c.table, c.lens)
     c.lens += torch.tensor([150, 1, 30], dtype=torch.int32, device="cuda") - 2
+    assert c.lens.tolist() == [168, -1, 128]     # the second row has no request: its outputs are not written
     for dtype in (torch.bfloat16, torch.float32):
-        got += la.softmax_decode_paged(q[:3], k[:3], v[:3], c.k, c.v, c.table, c.lens, out_dtype=dtype)
+        out, lse = la.softmax_decode_paged(q[:3], k[:3], v[:3], c.k, c.v, c.table, c.lens, out_dtype=dtype)
+        got += [out[[0, 2]], lse[[0, 2]]]
     fp32, l2 = torch.zeros(3, 8, 128, device="cuda"), torch.zeros(3, 8, device="cuda")
     la.softmax_decode_paged(q[:3], k[:3], v[:3], c.k, c.v, c.table, c.lens, out=fp32, lse=l2)
     la.cache_copy_pages(c.k, c.v, c.table[0, :1].clone(), c.table[0, 3:4].clone())

@@ -114,10 +114,11 @@ def test_workspaces(L):
     need = L.la_softmax_prefill_paged_workspace_size(1, BIG, 8, 2, 128)
     assert chunk(L, T=BIG, longest=BIG, n=need - 1, n_pages=1 << 16, max_pages=1 << 15) == WORKSPACE
     size = L.la_softmax_decode_paged_workspace_size
-    assert size(4, 8, 2, 128, 16, 5) == 0           # few short rows: none needed
-    need = size(400, 8, 2, 128, 16, 5)
+    assert size(4, 8, 2, 128, 16, 5) == size(400, 8, 2, 128, 16, 5) == 0   # short rows: none needed
+    need = size(400, 8, 2, 128, 128, 512)
     assert need > 0 and size(1, 8, 2, 128, 128, 4096) == need
-    assert decode(L, B=400, n=need - 1) == WORKSPACE and decode(L, B=400, ws=0) == WORKSPACE
+    long = dict(B=400, page=128, max_pages=512)
+    assert decode(L, n=need - 1, **long) == WORKSPACE and decode(L, ws=0, **long) == WORKSPACE
 
 
 def test_decode_and_copies(L):
