@@ -62,7 +62,8 @@ constexpr int SMX_SLOTS = 4;                                // item queue
 constexpr float RESCALE_LOG2 = 8.f;
 
 // Entries: the row blocks of every sequence, sequence by sequence, each from
-// its last block (the longest row of keys) to its first.
+// its last block (the longest row of keys) to its first, or (by_length) those of
+// all sequences from the longest row of keys to the shortest.
 struct SoftmaxScheduleParams {
     const int *cu;            // device cu_seqlens [nseq + 1]
     const int *past;          // device [nseq] cached tokens, or null (none)
@@ -70,6 +71,7 @@ struct SoftmaxScheduleParams {
     long long max_keys;       // bound on past + new tokens of a sequence (paged)
     int rows;                 // rows per entry: 128 or 256
     int items_per_entry;
+    int by_length;
     int *hdr;                 // workspace header
     int *prefix;              // [nseq + 1] entries before each sequence
     int4 *entries;            // {sequence, first token, length, block}
@@ -95,6 +97,7 @@ struct SoftmaxPrefillParams {
     int H, Hkv, G;
     int pairs;                // pairs of query tiles per entry
     int rows;
+    int by_length;            // entries are in order of length: all heads of an entry in turn
     float scale_log2;         // scale * log2(e)
     unsigned long long wait_limit_ns;
     int *status;
@@ -387,12 +390,21 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
                         rest = blockIdx.x % (p.Hkv * p.pairs);
                         kvh = rest / p.pairs;
                     } else {
-                        // key/value head outermost, so that the CTAs at work share its keys in L2
                         t = atomicAdd(&p.hdr[HDR_TICKET], 1);
-                        const int per_head = max(1, ne * p.pairs);
-                        kvh = t / per_head;
-                        rest = t - kvh * per_head;
-                        if (t < total) own = p.entries[rest / p.pairs];
+                        int e;
+                        if (p.by_length) {
+                            const int per_entry = p.Hkv * p.pairs;
+                            e = t / per_entry;
+                            rest = t - e * per_entry;
+                            kvh = rest / p.pairs;
+                        } else {
+                            // key/value head outermost, so that the CTAs at work share its keys in L2
+                            const int per_head = max(1, ne * p.pairs);
+                            kvh = t / per_head;
+                            rest = t - kvh * per_head;
+                            e = rest / p.pairs;
+                        }
+                        if (t < total) own = p.entries[e];
                     }
                     cb->item[slot][SI_VALID] = t < total;
                     if (t < total) smx_item(kvh, own, rest % p.pairs, p, cb->item[slot]);
@@ -725,6 +737,61 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+// Entries of at most SCHED_THREADS sequences of at most SCHED_THREADS blocks each,
+// by block number (which is what a query block has keys before it, in blocks)
+// from the largest down: with m(w) sequences of more than w blocks, block w's
+// entries are the m(w) longest sequences'.
+__device__ __forceinline__ void schedule_by_length(const SoftmaxScheduleParams &s, int tid) {
+    __shared__ int nb[SCHED_THREADS], order[SCHED_THREADS], first[SCHED_THREADS + 1], warp_sums2[SCHED_THREADS / 32];
+    int n = 0;
+    if (tid < s.nseq) {
+        n = (s.cu[tid + 1] - s.cu[tid] + s.rows - 1) / s.rows;
+        nb[tid] = n;
+    }
+    __syncthreads();
+    if (tid < s.nseq) {
+        int rank = 0;
+        for (int j = 0; j < s.nseq; ++j) rank += nb[j] > n || (nb[j] == n && j < tid);
+        order[rank] = tid;
+    }
+    __syncthreads();
+    // thread x stands for block w = SCHED_THREADS - 1 - x: m(w), then a scan over x
+    const int w = SCHED_THREADS - 1 - tid;
+    int lo = 0, hi = s.nseq;  // the first of the ordered sequences with no more than w blocks
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (nb[order[mid]] > w) lo = mid + 1;
+        else hi = mid;
+    }
+    int x = lo;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if ((tid & 31) >= o) x += y;
+    }
+    if ((tid & 31) == 31) warp_sums2[tid >> 5] = x;
+    __syncthreads();
+    for (int v = 0; v < (tid >> 5); ++v) x += warp_sums2[v];
+    first[tid] = x - lo;
+    if (tid == SCHED_THREADS - 1) first[SCHED_THREADS] = x;
+    __syncthreads();
+    const int ne = first[SCHED_THREADS];
+    for (int e = tid; e < ne; e += SCHED_THREADS) {
+        int a = 0, b = SCHED_THREADS - 1;  // the last x whose first entry is at or before e
+        while (a < b) {
+            const int mid = (a + b + 1) >> 1;
+            if (first[mid] <= e) a = mid;
+            else b = mid - 1;
+        }
+        const int seq = order[e - first[a]], at = s.cu[seq];
+        s.entries[e] = make_int4(seq, at, s.cu[seq + 1] - at, SCHED_THREADS - 1 - a);
+    }
+    if (tid == 0) {
+        s.hdr[HDR_G] = ne;
+        s.hdr[HDR_TOTAL] = ne * s.items_per_entry;
+    }
+}
+
 // Scheduler of the softmax kernels: checks cu_seqlens and the cached lengths,
 // writes the entries and resets the tickets.  One block.
 __global__ void __launch_bounds__(SCHED_THREADS, 1) la_softmax_schedule_kernel(const SoftmaxScheduleParams s) {
@@ -749,6 +816,10 @@ __global__ void __launch_bounds__(SCHED_THREADS, 1) la_softmax_schedule_kernel(c
         }
     }
     if (bad) return;
+    if (s.by_length) {
+        schedule_by_length(s, tid);
+        return;
+    }
     __syncthreads();
     for (int base = 0; base < s.nseq; base += SCHED_THREADS) {  // exclusive scan of entry counts
         const int i = base + tid;

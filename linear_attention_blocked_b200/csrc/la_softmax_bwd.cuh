@@ -35,6 +35,7 @@ struct SoftmaxBwdParams {
     const int4 *entries;
     int T, H, Hkv, G;
     int nparts;                   // CTAs that share a key block's query heads
+    int by_length;                // entries are in order of length: all heads of an entry in turn
     float scale, scale_log2;
     unsigned long long wait_limit_ns;
     int *status;
@@ -222,9 +223,10 @@ la_softmax_dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_cons
                 if (lane == 0) {
                     const int t = atomicAdd(&p.hdr[HDR_TICKET], 1);
                     if (t < total) {
-                        const int per_head = ne * p.nparts, kvh = t / per_head, rest = t - kvh * per_head;
-                        const int part = rest % p.nparts;
-                        const int4 en = p.entries[rest / p.nparts];
+                        const int per = (p.by_length ? p.Hkv : ne) * p.nparts, outer = t / per, rest = t - outer * per;
+                        const int inner = rest / p.nparts, part = rest - inner * p.nparts;
+                        const int kvh = p.by_length ? inner : outer;
+                        const int4 en = p.entries[p.by_length ? outer : inner];
                         im[BI_VALID] = 1;
                         im[BI_TOK0] = en.y;
                         im[BI_LEN] = en.z;
@@ -601,8 +603,10 @@ la_softmax_dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                 if (lane == 0) {
                     const int t = atomicAdd(&p.hdr[HDR_TICKET2], 1);
                     if (t < total) {
-                        const int per_head = ne * p.G, kvh = t / per_head, rest = t - kvh * per_head;
-                        const int4 en = p.entries[rest / p.G];
+                        const int per = (p.by_length ? p.Hkv : ne) * p.G, outer = t / per, rest = t - outer * per;
+                        const int inner = rest / p.G;
+                        const int kvh = p.by_length ? inner : outer;
+                        const int4 en = p.entries[p.by_length ? outer : inner];
                         im[BI_VALID] = 1;
                         im[BI_TOK0] = en.y;
                         im[BI_LEN] = en.z;

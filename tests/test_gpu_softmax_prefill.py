@@ -116,3 +116,18 @@ def test_rejected_calls():
             la.softmax_prefill_varlen(q, k, v, cu_dev, 64, scale=scale)
     with pytest.raises(la.LAError):
         la.softmax_prefill_varlen(q, k, v, cu_dev, 64, out=q)
+
+
+def test_both_orders_of_the_work():
+    """Items by length (few tokens) and by head (many), with empty sequences and
+    lengths that tie, give the same rows."""
+    lens = [130, 0, 700, 129, 700, 1, 0, 1025]
+    for H, Hkv in ((64, 64), (64, 8), (9, 3)):
+        run_and_check(lens, H, Hkv, seed=31)
+    # 2200 tokens of 64 key/value heads and more go head by head
+    q, k, v, cu, cu_dev = packed([2000, 3, 300], 64, 64, 33)
+    out, lse = la.softmax_prefill_varlen(q, k, v, cu_dev, 2000)
+    assert la.get_device_status() == la.LA_OK
+    for a, b in zip(cu[:-1], cu[1:]):
+        check(out[a:b, :2], lse[a:b, :2], attention64(q[a:b, :2], k[a:b, :2], v[a:b, :2], 0, S), b - a)
+        check(out[a:b, -1:], lse[a:b, -1:], attention64(q[a:b, -1:], k[a:b, -1:], v[a:b, -1:], 0, S), b - a)
