@@ -496,7 +496,7 @@ LA_API la_status la_softmax_prefill_backward_varlen(const void *q, const void *k
  * not overlap the other buffers.
  * ------------------------------------------------------------------------- */
 LA_API size_t la_softmax_prefill_paged_workspace_size(int nseq, int total_tokens, int H, int Hkv,
-                                                      int d);
+                                                      int d, int page_size, int max_pages);
 
 LA_API la_status la_softmax_prefill_paged(const void *q, const void *k, const void *v,
                                           const int *cu_seqlens, int nseq, int total_tokens,

@@ -121,7 +121,7 @@ def lib():
         L.la_softmax_prefill_backward_varlen.argtypes = [vp, vp, vp, vp, vp, vp, vp, c_int, c_int, c_int, c_int, c_int,
                                                          c_int, f32, vp, vp, vp, vp, sz, vp]
         L.la_softmax_prefill_backward_varlen.restype = c_int
-        L.la_softmax_prefill_paged_workspace_size.argtypes = [c_int] * 5
+        L.la_softmax_prefill_paged_workspace_size.argtypes = [c_int] * 7
         L.la_softmax_prefill_paged_workspace_size.restype = sz
         L.la_softmax_prefill_paged.argtypes = [vp, vp, vp, vp, c_int, c_int, c_int, c_int, c_int, c_int, f32, vp, vp,
                                                c_int, c_int, vp, c_int, vp, vp, vp, vp, sz, vp]

@@ -172,7 +172,7 @@ PyObject *prefill_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (want < 0) Py_RETURN_NONE;
         if ((a[11] != Py_None || want) && !output(a[11], lse, {x.T, x.H}, FP32, x.dev)) Py_RETURN_NONE;
         const int nseq = (int)cu.size(0) - 1;
-        const size_t bytes = la_softmax_prefill_paged_workspace_size(nseq, x.T, x.H, x.Hkv, x.d);
+        const size_t bytes = la_softmax_prefill_paged_workspace_size(nseq, x.T, x.H, x.Hkv, x.d, c.page, c.max_pages);
         if (bytes) ws = make({(int64_t)bytes}, at::kByte, x.dev);
         const la_status st = la_softmax_prefill_paged(
             x.q.ptr(), x.k.ptr(), x.v.ptr(), (const int *)cu.ptr(), nseq, x.T, longest, x.H, x.Hkv, x.d, scale, c.k.ptr(),

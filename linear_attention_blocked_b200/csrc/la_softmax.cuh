@@ -53,13 +53,15 @@ constexpr int SMX_STAGES = 5;
 constexpr int SMX_Q = 0;
 constexpr int SMX_KV = 2 * TILE_BYTES;
 constexpr int SMX_CTRL = SMX_KV + SMX_STAGES * TILE_BYTES;
-constexpr int SMX_STAT = SMX_CTRL + 512;                    // {c m, l} of both tiles' rows
+constexpr int SMX_STAT = SMX_CTRL + 576;                    // {c m, l} of both tiles' rows
 constexpr int SMX_SMEM = SMX_STAT + 2 * BLK * 8;            // (1024-byte aligned as it is)
 static_assert(SMX_SMEM <= 227 * 1024, "shared memory of one CTA");
 constexpr uint32_t SMX_TM_S = 0, SMX_TM_O = 256;            // tile t: + 128 t
 constexpr int HDR_TICKET2 = 3;                              // second ticket counter of the workspace header
 constexpr int SMX_SLOTS = 4;                                // item queue
 constexpr float RESCALE_LOG2 = 8.f;
+constexpr int SMX_CTAS = 148;                               // split: runs of key tiles
+constexpr int SMX_PART = D + 4;                             // floats of a row's part: O, c m, l
 
 // Entries: the row blocks of every sequence, sequence by sequence, each from
 // its last block (the longest row of keys) to its first, or (by_length) those of
@@ -86,8 +88,11 @@ struct SoftmaxPrefillParams {
     const int *past;          // device [nseq] or null
     const int *pages;         // device [nseq, max_pages] page table, or null (no cache)
     int max_pages, n_pages, page, page_shift;
-    // direct: every CTA has one item at most and finds it in cu itself
-    int direct;
+    // direct: every CTA has one item at most and finds it in cu itself; split: it
+    // has a run of key tiles, equal to the others', of whichever items they are of
+    int direct, split;
+    float *parts;             // split: [SMX_CTAS][2][2 tiles][128][SMX_PART] O, m, l of cut items
+    int4 *info;               // split: [SMX_CTAS][3] the item cut at the CTA's end
     const int *cu;            // device [nseq + 1] (direct, append)
     int nseq, T, max_seqlen;
     long long max_keys;       // room of a sequence's pages
@@ -104,9 +109,10 @@ struct SoftmaxPrefillParams {
 };
 
 // item fields
-enum { SI_VALID = 0, SI_H0, SI_H1, SI_B0, SI_B1, SI_N0, SI_N1, SI_TOK0, SI_LEN, SI_PAST, SI_KVH, SI_SEQ, SI_FIELDS };
+enum { SI_VALID = 0, SI_H0, SI_H1, SI_B0, SI_B1, SI_N0, SI_N1, SI_TOK0, SI_LEN, SI_PAST, SI_KVH, SI_SEQ, SI_J0, SI_PART, SI_FIELDS };
 // N0, N1: key tiles of the two query tiles: those of the cached tokens, then those
-// of the new ones up to the query tile's own rows
+// of the new ones up to the query tile's own rows.  A piece of an item (split) has
+// N0, N1 of them from tile J0 on; PART: the slot for its part of the sums, or -1.
 
 struct SoftmaxCtrl {
     uint64_t kv_full[SMX_STAGES], kv_empty[SMX_STAGES];
@@ -120,12 +126,12 @@ struct SoftmaxCtrl {
     uint64_t item_full[SMX_SLOTS];    // [1]
     uint64_t item_empty[SMX_SLOTS];   // [14] Q, MMA, 8 softmax and 4 output warps
     uint64_t fin;                     // [1] tear-down: every MMA done
-    int item[SMX_SLOTS][12];
+    int item[SMX_SLOTS][16];
     uint32_t tmem_base;
     volatile int abort;
 };
-static_assert(sizeof(SoftmaxCtrl) <= 512, "control block");
-static_assert(SI_FIELDS <= 12, "item fields");
+static_assert(sizeof(SoftmaxCtrl) <= 576, "control block");
+static_assert(SI_FIELDS <= 16, "item fields");
 
 // Programmatic dependent launch: wait for the kernel before this one in the
 // stream to end (when it was launched so; else a no-op); let the next one start.
@@ -212,6 +218,8 @@ __device__ __forceinline__ void smx_item(int kvh, int4 en, int pair, const Softm
     item[SI_PAST] = past;
     item[SI_KVH] = kvh;
     item[SI_SEQ] = en.x;
+    item[SI_J0] = 0;
+    item[SI_PART] = -1;
 }
 
 // Is sequence i of the tables as the header asks?
@@ -259,6 +267,130 @@ __device__ __forceinline__ int smx_find(int e, int lane, const SoftmaxPrefillPar
         return 0;
     }
     return at;
+}
+
+// Split: the key tiles of all items are laid end to end, entry by entry, all items
+// of an entry with as many tiles as its longest, and cut into equal runs.
+struct SplitCursor {
+    int seq, blk, tok0, len, past, cost;  // the entry, and tiles of each of its items
+    int rest, j;                          // item of the entry, tile of the item
+    int n;                                // CTAs with a run
+    long long u, u1, total;               // this run's place and end among all tiles
+};
+
+__device__ __forceinline__ int smx_cost(int blk, int len, int past, int bpe) {
+    return (past + BLK - 1) / BLK + min((blk + 1) * bpe, (len + BLK - 1) / BLK);
+}
+
+// A warp finds its CTA's run; false without one.  Checks the tables like smx_find.
+__device__ __forceinline__ bool smx_split(SplitCursor &c, int lane, const SoftmaxPrefillParams &p) {
+    const int bpe = p.rows / BLK;
+    const long long hp = (long long)p.Hkv * p.pairs;
+    bool bad = lane == 0 && (p.cu[0] != 0 || p.cu[p.nseq] != p.T);
+    long long at = 0;
+    c.total = 0;
+    for (int pass = 0; pass < 2; ++pass) {  // the sum, then the run's first entry
+        for (int base = 0; base < p.nseq; base += 32) {
+            const int i = base + lane;
+            long long mine = 0;
+            int a = 0, len = 0, past = 0;
+            if (i < p.nseq) {
+                a = p.cu[i];
+                const int b = p.cu[i + 1];
+                if (smx_sequence_ok(i, a, b, p.past, p.T, p.max_seqlen, p.max_keys)) {
+                    len = b - a;
+                    past = p.past && len ? p.past[i] : 0;
+                } else {
+                    bad = true;
+                }
+                for (int blk = 0; blk < (len + p.rows - 1) / p.rows; ++blk) mine += smx_cost(blk, len, past, bpe);
+            }
+            long long incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            if (pass == 0) {
+                c.total += __shfl_sync(0xffffffffu, incl, 31) * hp;
+                continue;
+            }
+            const long long first = (at + incl - mine) * hp;
+            const uint32_t hit = __ballot_sync(0xffffffffu, c.u >= first && c.u < first + mine * hp);
+            at += __shfl_sync(0xffffffffu, incl, 31);
+            if (!hit) continue;
+            const int src = __ffs(hit) - 1;
+            c.seq = base + src;
+            c.tok0 = __shfl_sync(0xffffffffu, a, src);
+            c.len = __shfl_sync(0xffffffffu, len, src);
+            c.past = __shfl_sync(0xffffffffu, past, src);
+            long long rem = c.u - __shfl_sync(0xffffffffu, first, src);
+            for (c.blk = (c.len + p.rows - 1) / p.rows - 1;; --c.blk) {
+                c.cost = smx_cost(c.blk, c.len, c.past, bpe);
+                if (rem < c.cost * hp) break;
+                rem -= c.cost * hp;
+            }
+            c.rest = (int)(rem / c.cost);
+            c.j = (int)(rem % c.cost);
+            return true;
+        }
+        if (pass == 0) {
+            if (__any_sync(0xffffffffu, bad)) {
+                if (lane == 0) record_status(p.status, ST_INVALID);
+                return false;
+            }
+            // (a run of less than four tiles would not pay)
+            c.n = (int)min((long long)gridDim.x, (c.total + 3) / 4);
+            if ((int)blockIdx.x >= c.n) return false;
+            c.u = c.total * blockIdx.x / c.n;
+            c.u1 = c.total * (blockIdx.x + 1) / c.n;
+        }
+    }
+    return false;
+}
+
+// The run's next piece into `item` (one thread); false at its end.
+__device__ __forceinline__ bool smx_piece(SplitCursor &c, const SoftmaxPrefillParams &p, int *item) {
+    const int bpe = p.rows / BLK;
+    while (c.u < c.u1) {
+        const int j0 = c.j, take = (int)min((long long)(c.cost - c.j), c.u1 - c.u);
+        smx_item(c.rest / p.pairs, make_int4(c.seq, c.tok0, c.len, c.blk), c.rest % p.pairs, p, item);
+        const int n0 = item[SI_N0], n1 = item[SI_N1], nmax = max(n0, n1);
+        const long long begin = c.u - j0;  // the item's first tile among all
+        c.u += take;
+        c.j += take;
+        if (c.j == c.cost) {
+            c.j = 0;
+            if (++c.rest == p.Hkv * p.pairs && c.u < c.u1) {
+                c.rest = 0;
+                if (--c.blk < 0) {
+                    do {
+                        ++c.seq;
+                        c.tok0 = p.cu[c.seq];
+                        c.len = p.cu[c.seq + 1] - c.tok0;
+                    } while (c.len == 0);
+                    c.past = p.past ? p.past[c.seq] : 0;
+                    c.blk = (c.len + p.rows - 1) / p.rows - 1;
+                }
+                c.cost = smx_cost(c.blk, c.len, c.past, bpe);
+            }
+        }
+        if (j0 >= nmax) continue;  // this item has fewer tiles than the entry's longest
+        item[SI_N0] = max(0, min(n0 - j0, take));
+        item[SI_N1] = max(0, min(n1 - j0, take));
+        item[SI_J0] = j0;
+        if (j0 == 0 && take >= nmax) return true;  // whole
+        item[SI_PART] = j0 == 0 ? 1 : 0;           // (a run cuts one item at either end)
+        if (j0 == 0) {
+            const int parts = (int)(((begin + nmax) * c.n - 1) / c.total) - (int)blockIdx.x + 1;
+            int4 *in = p.info + 3 * blockIdx.x;
+            in[0] = make_int4(parts, item[SI_TOK0], item[SI_LEN], 0);
+            in[1] = make_int4(item[SI_H0], item[SI_H1], item[SI_B0], item[SI_B1]);
+            in[2] = make_int4(n0, n1, 0, 0);
+        }
+        return true;
+    }
+    return false;
 }
 
 // The pages that hold keys [key0, key0 + 128) of a sequence with `keys` cached
@@ -368,9 +500,13 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
             const uint64_t pol = policy_evict_last();
             int total = 0, ne = 0;
             int4 own = make_int4(0, 0, 0, 0);
+            SplitCursor run;
             pdl_wait();    // what came before has ended: inputs and, when not direct, tables
             pdl_launch();  // the kernel behind may be set up (it waits for this one's end)
-            if (p.direct) {
+            if (p.split) {
+                if (lane == 0) p.info[3 * blockIdx.x] = make_int4(0, 0, 0, 0);
+                total = smx_split(run, lane, p) ? 0x7fffffff : 0;
+            } else if (p.direct) {
                 const int e = blockIdx.x / (p.Hkv * p.pairs);
                 total = e < smx_find(e, lane, p, own) ? 1 : 0;
             } else {
@@ -383,7 +519,10 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
                 const int slot = it % SMX_SLOTS;
                 if (!wait(&cb->item_empty[slot], ((it / SMX_SLOTS) & 1) ^ 1)) { ok = false; break; }
                 int t = 0;
-                if (lane == 0) {
+                if (lane == 0 && p.split) {
+                    if (total == 0 || !smx_piece(run, p, cb->item[slot])) t = total;
+                    cb->item[slot][SI_VALID] = t < total;
+                } else if (lane == 0) {
                     int kvh, rest;
                     if (p.direct) {
                         t = (int)it;
@@ -414,12 +553,13 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
                 const int n0 = cb->item[slot][SI_N0], n1 = cb->item[slot][SI_N1];
                 const int kvh = cb->item[slot][SI_KVH], tok0 = cb->item[slot][SI_TOK0];
                 const int past = cb->item[slot][SI_PAST], seq = cb->item[slot][SI_SEQ];
+                const int j0 = cb->item[slot][SI_J0];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&cb->item_full[slot]);
                 ++it;
                 if (t >= total) break;
                 const int nmax = max(n0, n1), np = (past + BLK - 1) / BLK;
-                for (int j = 0; j < nmax && ok; ++j) {
+                for (int j = j0; j < j0 + nmax && ok; ++j) {
                     int pid = 0;
                     if (j < np) {
                         const int i = (j << (7 - p.page_shift)) + lane;  // page of this lane in the tile
@@ -463,7 +603,7 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
             // bit t: phase of the tile's Q, P and O barriers
             uint32_t qph = 0, pph = 0, oph = 0;
             uint32_t pend = 3;                 // bit t: first scores of the tile's next item not issued yet
-            constexpr uint32_t MASK = 1u << SI_N0 | 1u << SI_N1 | 1u << SI_PAST | 1u << SI_LEN;
+            constexpr uint32_t MASK = 1u << SI_N0 | 1u << SI_N1 | 1u << SI_PAST | 1u << SI_LEN | 1u << SI_J0;
             bool ok = smx_next<MASK>(it, cur, lane, p, cb);
             // S_t of step j of an item whose first K tile is at ring position rb
             auto scores = [&](int t, const int (&im)[SI_FIELDS], uint32_t rb, int j) -> bool {
@@ -486,7 +626,9 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
             };
             while (ok) {
                 const int n0 = cur[SI_N0], n1 = cur[SI_N1], nmax = max(n0, n1);
-                const int np = (cur[SI_PAST] + BLK - 1) / BLK;
+                // tile j of the piece is tile j + J0 of the item: cached keys up to np
+                const int np = (cur[SI_PAST] + BLK - 1) / BLK - cur[SI_J0];
+                const int past = cur[SI_PAST] - cur[SI_J0] * BLK;
                 bool have_nxt = false, nxt_valid = false;
                 for (int t = 0; t < 2 && ok; ++t) {
                     if (((pend >> t) & 1) && (t ? n1 : n0) > 0) {
@@ -501,7 +643,7 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
                         const uint32_t pos = base + 2 * j + 1, s = pos % SMX_STAGES;
                         uint8_t *vp = smem + SMX_KV + s * TILE_BYTES;
                         if (!wait(&cb->kv_full[s], (pos / SMX_STAGES) & 1)) { ok = false; break; }
-                        const int valid = j < np ? cur[SI_PAST] - j * BLK : cur[SI_LEN] - (j - np) * BLK;
+                        const int valid = j < np ? past - j * BLK : cur[SI_LEN] - (j - np) * BLK;
                         if (valid < BLK && (t == 0 || j >= n0)) {
                             // rows behind the last key meet P = 0, which keeps out what they
                             // hold only if it is finite: zero them
@@ -535,7 +677,9 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
                                 if (cb->abort) ok = false;
                             }
                             pend |= 1u << t;
-                            if (ok && nxt_valid && (t ? nxt[SI_N1] : nxt[SI_N0]) > 0) {
+                            // (tile 0's scores come first: tile 1's release the K tile)
+                            const bool behind = t == 1 && (pend & 1) && nxt[SI_N0] > 0;
+                            if (ok && nxt_valid && !behind && (t ? nxt[SI_N1] : nxt[SI_N0]) > 0) {
                                 ok = scores(t, nxt, base + 2 * nmax, 0);
                                 pend &= ~(1u << t);
                             }
@@ -604,11 +748,14 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
         uint32_t it = 0, sn = 0, in = 0;
         int im[SI_FIELDS];
         bool ok = true;
-        constexpr uint32_t MASK = 1u << SI_N0 | 1u << SI_N1 | 1u << SI_B0 | 1u << SI_B1 | 1u << SI_PAST;
+        constexpr uint32_t MASK = 1u << SI_N0 | 1u << SI_N1 | 1u << SI_B0 | 1u << SI_B1 | 1u << SI_PAST | 1u << SI_J0;
         while (ok && smx_next<MASK>(it, im, lane, p, cb)) {
             const int nt = t ? im[SI_N1] : im[SI_N0];
             if (nt == 0) continue;
-            const int past = im[SI_PAST], np = (past + BLK - 1) / BLK;
+            // tile j of the piece is tile j + J0 of the item: cached keys up to np, then new
+            // ones up to the diagonal
+            const int past = im[SI_PAST] - im[SI_J0] * BLK, np = (im[SI_PAST] + BLK - 1) / BLK - im[SI_J0];
+            const int diag = np + (t ? im[SI_B1] : im[SI_B0]);
             float m = -INFINITY, l = 0.f;           // m: maximum in use
             for (int j = 0; j < nt; ++j) {
                 if (!wait(&cb->s_full[t], sn & 1)) { ok = false; break; }
@@ -616,7 +763,7 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
                 uint32_t x[128];
                 tmem_ld_cols<128>(ts, x);
                 // the last tile of cached keys may be ragged, that of the own rows is the diagonal
-                if (j == nt - 1 || (j < np && past - j * BLK < BLK)) {
+                if (j == diag || (j < np && past - j * BLK < BLK)) {
                     const int lim = j < np ? past - j * BLK - 1 : r;  // columns [0, lim] are seen
 #pragma unroll
                     for (int i = 0; i < 128; ++i)
@@ -691,7 +838,13 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
         while (ok && smx_next<MASK>(it, im, lane, p, cb)) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                if ((t ? im[SI_N1] : im[SI_N0]) == 0) continue;
+                // a part of a cut item goes to the workspace, as it is
+                float *part = im[SI_PART] < 0 ? nullptr
+                    : p.parts + (((size_t)blockIdx.x * 2 + im[SI_PART]) * 2 + t) * BLK * SMX_PART + (size_t)r * SMX_PART;
+                if ((t ? im[SI_N1] : im[SI_N0]) == 0) {
+                    if (part) *reinterpret_cast<float2 *>(part + D) = make_float2(-INFINITY, 0.f);  // none of the tile's keys
+                    continue;
+                }
                 const float2 *stat = reinterpret_cast<const float2 *>(smem + SMX_STAT) + t * BLK;
                 if (!wait(&cb->stat_full[t], n[t] & 1)) { ok = false; break; }
                 const float2 ml = stat[r];
@@ -709,7 +862,12 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
                     uint32_t o[32];
                     __syncwarp();
                     tmem_ld_wait32(trow + SMX_TM_O + t * 128 + q * 32, o);
-                    if (mine) {
+                    if (mine && part) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            reinterpret_cast<uint4 *>(part + q * 32)[i] =
+                                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    } else if (mine) {
                         uint4 *to = reinterpret_cast<uint4 *>(p.out + at * D + q * 32);
                         scale32(o, inv);
 #pragma unroll
@@ -725,7 +883,8 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&cb->o_empty[t]);
-                if (mine && p.lse) p.lse[at] = (ml.x + log2f(ml.y)) * 0.69314718055994531f;  // ln 2
+                if (part) *reinterpret_cast<float2 *>(part + D) = ml;
+                else if (mine && p.lse) p.lse[at] = (ml.x + log2f(ml.y)) * 0.69314718055994531f;  // ln 2
             }
         }
     }
@@ -735,6 +894,64 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Split: joins the parts of the items that the runs' borders cut.  Block (c, tile,
+// z) has rows 8 z to 8 z + 7, a warp each, of the item that starts in CTA c's run
+// and goes on, if one does; a lane has four features, and the m and l of every
+// 32nd part.
+constexpr int SPLIT_JOIN_ROWS = 8;
+
+__global__ void __launch_bounds__(32 * SPLIT_JOIN_ROWS)
+la_softmax_split_join_kernel(const __grid_constant__ SoftmaxPrefillParams p) {
+    pdl_wait();
+    pdl_launch();
+    const int c = blockIdx.x, t = blockIdx.y, lane = threadIdx.x & 31;
+    const int r = blockIdx.z * SPLIT_JOIN_ROWS + (threadIdx.x >> 5);
+    const int4 a = p.info[3 * c], hb = p.info[3 * c + 1], n = p.info[3 * c + 2];
+    if (a.x == 0) return;
+    const int h = t ? hb.y : hb.x, row = (t ? hb.w : hb.z) * BLK + r;
+    if ((t ? n.y : n.x) == 0 || row >= a.z) return;
+    // first part: slot 1 of CTA c; the others: slot 0 of the CTAs behind it
+    auto part = [&](int i) -> const float * {
+        return p.parts + (((size_t)(c + i) * 2 + (i == 0)) * 2 + t) * BLK * SMX_PART + (size_t)r * SMX_PART;
+    };
+    float m = -INFINITY, l = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int base = 0; base < a.x; base += 32) {
+        const int i = base + lane, count = min(32, a.x - base);
+        const float2 ml = i < a.x ? *reinterpret_cast<const float2 *>(part(i) + D) : make_float2(-INFINITY, 0.f);
+        float mm = fmaxf(m, ml.x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+        const float u = mm == -INFINITY ? 0.f : mm;
+        const float old = m == -INFINITY ? 0.f : ex2(m - u), w = ml.x == -INFINITY ? 0.f : ex2(ml.x - u);
+        float s = ml.y * w;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        l = fmaf(l, old, s);
+        m = mm;
+        x.x *= old;
+        x.y *= old;
+        x.z *= old;
+        x.w *= old;
+#pragma unroll 8
+        for (int k = 0; k < count; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            if (wk != 0.f) {  // (a part without keys of this tile holds nothing)
+                const float4 o = reinterpret_cast<const float4 *>(part(base + k))[lane];
+                x.x = fmaf(o.x, wk, x.x);
+                x.y = fmaf(o.y, wk, x.y);
+                x.z = fmaf(o.z, wk, x.z);
+                x.w = fmaf(o.w, wk, x.w);
+            }
+        }
+    }
+    const size_t at = ((size_t)a.y + row) * p.H + h;
+    const float inv = 1.f / l;
+    reinterpret_cast<uint2 *>(p.out + at * D)[lane] =
+        make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+    if (lane == 0 && p.lse) p.lse[at] = (m + log2f(l)) * 0.69314718055994531f;  // ln 2
 }
 
 // Entries of at most SCHED_THREADS sequences of at most SCHED_THREADS blocks each,

@@ -26,21 +26,35 @@ SoftmaxLayout softmax_layout(int nseq, long long T) {
 
 // Work items of the prompt kernel: pairs of query tiles.  With no more items
 // than SMs every CTA has one at most, which it finds itself: no scheduler launch
-// and no workspace (129 tokens, 64 heads over 8: 14.4 us with, 12.3 us without; back to back, with the next call set up meanwhile, 10.2 us).
+// and no workspace (129 tokens, 64 heads over 8: 14.4 us with, 12.3 us without; back
+// to back, with the next call set up meanwhile, 10.2 us).
 // Depends on the shape only, so that the workspace size does.
 struct SoftmaxItems {
     int rows, pairs;   // rows per entry, pairs per entry and key/value head
     long long items;
     bool direct;
+    bool split;
 };
 
-SoftmaxItems softmax_items(int nseq, long long T, int H, int Hkv) {
+// With few items of many key tiles the tiles are cut into equal runs, one per SM,
+// and cut items joined by a second kernel.  Whole items / runs, us: 16 new tokens,
+// 64 heads over 8, behind 2000 35 / 23, behind 16000 215 / 63; 128 behind 60000 787 /
+// 243; 256 behind 8000 118 / 83; a prompt of 8000, 2 heads 111 / 57.  From 100 items on
+// the runs are hardly shorter than the items (500 behind 8000, 128 items: 123 / 161),
+// and below 14 tiles the second launch costs what they save (prompt of 1600, 8 heads
+// over 1: 29 / 32).
+constexpr size_t kSplitParts = (size_t)la::SMX_CTAS * 2 * 2 * la::BLK * la::SMX_PART * sizeof(float);
+constexpr size_t kSplitWs = kSplitParts + (size_t)la::SMX_CTAS * 3 * sizeof(int4);
+
+// keys: a bound on the keys of a row
+SoftmaxItems softmax_items(int nseq, long long T, long long keys, int H, int Hkv) {
     const int G = H / Hkv;
     SoftmaxItems s;
     s.rows = G % 2 ? 2 * la::BLK : la::BLK;
     s.pairs = G % 2 ? G : G / 2;
     s.items = (T / s.rows + nseq) * Hkv * s.pairs;
     s.direct = T > 0 && s.items <= 148;
+    s.split = s.direct && s.items <= 96 && keys > 13 * la::BLK;
     return s;
 }
 
@@ -176,13 +190,15 @@ la_status softmax_prefill_impl(const void *q, const void *k, const void *v, cons
                   ranges_overlap(cache->k, in.n_cache, v, n_kv) || ranges_overlap(cache->v, in.n_cache, q, n_q) ||
                   ranges_overlap(cache->v, in.n_cache, k, n_kv) || ranges_overlap(cache->v, in.n_cache, v, n_kv)))
         return LA_ERR_INVALID_ARGUMENT;
-    const SoftmaxItems it = softmax_items(nseq, T, H, Hkv);
+    const long long max_keys = cache ? (long long)cache->max_pages * cache->page : 0;
+    const SoftmaxItems it = softmax_items(nseq, T, cache ? max_keys : (max_seqlen < T ? max_seqlen : T), H, Hkv);
     const SoftmaxLayout w = softmax_layout(nseq, T);
-    if (!it.direct) {
-        if (!workspace || ws_bytes < w.total) return LA_ERR_WORKSPACE;
+    const size_t need = it.split ? kSplitWs : it.direct ? 0 : w.total;
+    if (need) {
+        if (!workspace || ws_bytes < need) return LA_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return LA_ERR_INVALID_ARGUMENT;
-        if (!clear_of(workspace, w.total, in) || ranges_overlap(workspace, w.total, out, n_q) ||
-            ranges_overlap(workspace, w.total, lse, n_lse))
+        if (!clear_of(workspace, need, in) || ranges_overlap(workspace, need, out, n_q) ||
+            ranges_overlap(workspace, need, lse, n_lse))
             return LA_ERR_INVALID_ARGUMENT;
     }
     const int G = H / Hkv, rows = it.rows, pairs = it.pairs;
@@ -193,7 +209,6 @@ la_status softmax_prefill_impl(const void *q, const void *k, const void *v, cons
     if (!status) return LA_ERR_CUDA;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
 
-    const long long max_keys = cache ? (long long)cache->max_pages * cache->page : 0;
     const int sms = device_sm_count();
     la::SoftmaxScheduleParams sp;
     sp.cu = cu;
@@ -265,6 +280,11 @@ la_status softmax_prefill_impl(const void *q, const void *k, const void *v, cons
     pp.wait_limit_ns = g_wait_limit_ns.load();
     pp.status = status;
     pp.direct = direct;
+    pp.split = it.split;
+    if (it.split) {
+        pp.parts = reinterpret_cast<float *>(ws);
+        pp.info = reinterpret_cast<int4 *>(ws + kSplitParts);
+    }
     pp.cu = cu;
     pp.nseq = nseq;
     pp.T = (int)T;
@@ -272,10 +292,19 @@ la_status softmax_prefill_impl(const void *q, const void *k, const void *v, cons
     pp.max_keys = max_keys;
     st = ensure_smem_attr(g_attr_softmax, la::la_softmax_prefill_kernel, la::SMX_SMEM);
     if (st != LA_OK) return st;
-    if (!launch_dependent(la::la_softmax_prefill_kernel, dim3((unsigned)(direct ? items : sms)), la::SMX_THREADS,
-                          la::SMX_SMEM, stream, mq, mk, mv, mkc, mvc, pp))
+    const long long grid = it.split ? la::SMX_CTAS : direct ? items : sms;
+    if (!launch_dependent(la::la_softmax_prefill_kernel, dim3((unsigned)grid), la::SMX_THREADS, la::SMX_SMEM, stream, mq,
+                          mk, mv, mkc, mvc, pp))
         return LA_ERR_CUDA;
     ++g_launches;
+    if (it.split) {
+        const int tile_rows = max_seqlen < la::BLK ? max_seqlen : la::BLK;
+        const unsigned z = (unsigned)(tile_rows + la::SPLIT_JOIN_ROWS - 1) / la::SPLIT_JOIN_ROWS;
+        if (!launch_dependent(la::la_softmax_split_join_kernel, dim3(la::SMX_CTAS, 2, z ? z : 1),
+                              32 * la::SPLIT_JOIN_ROWS, 0, stream, pp))
+            return LA_ERR_CUDA;
+        ++g_launches;
+    }
     return LA_OK;
 }
 
@@ -366,9 +395,20 @@ la_status launch_decode(int cluster, const CUtensorMap &mk, const CUtensorMap &m
 
 }  // namespace
 
+namespace {
+
+// Workspace of the prompt kernel for rows of up to `keys` keys: of a call that
+// knows a smaller bound at most this.
+size_t softmax_ws(int nseq, long long T, long long keys, int H, int Hkv) {
+    const SoftmaxItems it = softmax_items(nseq, T, keys, H, Hkv);
+    return it.split ? kSplitWs : it.direct ? 0 : softmax_layout(nseq, T).total;
+}
+
+}  // namespace
+
 size_t la_softmax_prefill_varlen_workspace_size(int nseq, int total_tokens, int H, int Hkv, int d) {
     if (nseq < 0 || total_tokens < 0 || check_softmax(H, Hkv, d, 1.f) != LA_OK) return 0;
-    return softmax_items(nseq, total_tokens, H, Hkv).direct ? 0 : softmax_layout(nseq, total_tokens).total;
+    return softmax_ws(nseq, total_tokens, total_tokens, H, Hkv);
 }
 
 la_status la_softmax_prefill_varlen(const void *q, const void *k, const void *v, const int *cu_seqlens, int nseq,
@@ -378,8 +418,11 @@ la_status la_softmax_prefill_varlen(const void *q, const void *k, const void *v,
                                 lse, workspace, ws_bytes, stream);
 }
 
-size_t la_softmax_prefill_paged_workspace_size(int nseq, int total_tokens, int H, int Hkv, int d) {
-    return la_softmax_prefill_varlen_workspace_size(nseq, total_tokens, H, Hkv, d);
+size_t la_softmax_prefill_paged_workspace_size(int nseq, int total_tokens, int H, int Hkv, int d, int page_size,
+                                               int max_pages) {
+    if (nseq < 0 || total_tokens < 0 || check_softmax(H, Hkv, d, 1.f) != LA_OK || page_size <= 0 || max_pages <= 0)
+        return 0;
+    return softmax_ws(nseq, total_tokens, (long long)page_size * max_pages, H, Hkv);
 }
 
 la_status la_softmax_prefill_paged(const void *q, const void *k, const void *v, const int *cu_seqlens, int nseq,

@@ -205,7 +205,8 @@ def _softmax_prefill_paged(q, k, v, cu_seqlens, max_seqlen, k_cache, v_cache, pa
     n_pages, page, max_pages = _cache(k_cache, v_cache, page_table, cache_lens, nseq, Hkv, d, dev)
     out = _like(out, "out", q, dev)
     lse = _rows(lse, want_lse, q, T, H, dev)
-    ws, at, nbytes = _scratch(workspace, _size("la_softmax_prefill_paged_workspace_size", nseq, T, H, Hkv, d), q, dev)
+    nbytes = _size("la_softmax_prefill_paged_workspace_size", nseq, T, H, Hkv, d, page, max_pages)
+    ws, at, nbytes = _scratch(workspace, nbytes, q, dev)
     _done(lib().la_softmax_prefill_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), nseq, T,
                                          max_seqlen, H, Hkv, d, SCALE if scale is None else scale, k_cache.data_ptr(),
                                          v_cache.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages,

@@ -193,3 +193,12 @@ def test_decode_in_every_form(heads):
         past = [(longest * 7919 * (i + 1)) % (longest + 1) for i in range(B)]
         past[-1] = longest
         decode(past, *heads, page=128 if longest > 1000 else 32, seed=B)
+
+
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("heads", [(8, 1), (1, 1), (6, 2), (16, 2)], ids=str)
+def test_chunks_behind_long_caches(heads, page):
+    """Few new tokens, many cached ones: equal runs of key tiles, cut items joined."""
+    chunk([5], [9000], *heads, page=page, seed=50 + page)
+    chunk([1, 0, 40, 130], [4000, 0, 2500, 1], *heads, page=page, seed=60 + page)
+    chunk([257], [6001], *heads, page=page, seed=70 + page)

@@ -131,3 +131,33 @@ def test_both_orders_of_the_work():
     for a, b in zip(cu[:-1], cu[1:]):
         check(out[a:b, :2], lse[a:b, :2], attention64(q[a:b, :2], k[a:b, :2], v[a:b, :2], 0, S), b - a)
         check(out[a:b, -1:], lse[a:b, -1:], attention64(q[a:b, -1:], k[a:b, -1:], v[a:b, -1:], 0, S), b - a)
+
+
+@pytest.mark.parametrize("heads", [(1, 1), (8, 1), (3, 3), (5, 1), (4, 2)], ids=str)
+@pytest.mark.parametrize("lens", [[1600], [3000], [5001], [1700, 1, 0, 900, 128]], ids=str)
+def test_few_heads_and_long_rows(lens, heads):
+    """Few items of many key tiles: equal runs of tiles, cut items joined."""
+    run_and_check(lens, *heads, seed=len(lens) * 10 + heads[0])
+
+
+def test_runs_of_tiles_repeat_and_refuse():
+    q, k, v, cu, cu_dev = packed([4000, 300], 4, 1, seed=41)
+    out, lse = la.softmax_prefill_varlen(q, k, v, cu_dev, 4000)
+    again, lse2 = la.softmax_prefill_varlen(q, k, v, cu_dev, 4000)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    held = torch.zeros_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        la.softmax_prefill_varlen(q, k, v, cu_dev, 4000, out=held, want_lse=False)
+    graph.replay()
+    graph.replay()
+    assert torch.equal(held, out)
+    for table in ([0, 4000, 4299], [0, 4301, 4300], [0, -1, 4300]):
+        held.fill_(3.0)
+        la.softmax_prefill_varlen(q, k, v, torch.tensor(table, dtype=torch.int32, device="cuda"), 4300, out=held)
+        assert la.get_device_status() == la.LA_ERR_INVALID_ARGUMENT
+        assert (held == 3.0).all()
+    # NaN in one sequence stays there, whichever runs its tiles fall into
+    q[4000:], k[4000:], v[4000:] = float("nan"), float("nan"), float("nan")
+    got, _ = la.softmax_prefill_varlen(q, k, v, cu_dev, 4000)
+    assert torch.equal(got[:4000], out[:4000])

@@ -111,7 +111,7 @@ def test_workspaces(L):
     assert prefill(L, T=BIG, longest=BIG, ws=6 * FAR + 16, n=need) == INVALID
     need = L.la_softmax_prefill_backward_varlen_workspace_size(1, 128, 8, 2, 128)
     assert backward(L, n=need - 1) == WORKSPACE and backward(L, ws=0) == WORKSPACE
-    need = L.la_softmax_prefill_paged_workspace_size(1, BIG, 8, 2, 128)
+    need = L.la_softmax_prefill_paged_workspace_size(1, BIG, 8, 2, 128, 16, 1 << 15)
     assert chunk(L, T=BIG, longest=BIG, n=need - 1, n_pages=1 << 16, max_pages=1 << 15) == WORKSPACE
     size = L.la_softmax_decode_paged_workspace_size
     assert size(4, 8, 2, 128, 16, 5) == size(400, 8, 2, 128, 16, 5) == 0   # short rows: none needed
