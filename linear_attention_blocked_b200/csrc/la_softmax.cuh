@@ -1011,12 +1011,10 @@ __device__ __forceinline__ void schedule_by_length(const SoftmaxScheduleParams &
 
 // Scheduler of the softmax kernels: checks cu_seqlens and the cached lengths,
 // writes the entries and resets the tickets.  One block.
-__global__ void __launch_bounds__(SCHED_THREADS, 1) la_softmax_schedule_kernel(const SoftmaxScheduleParams s) {
+__device__ __forceinline__ void softmax_schedule(const SoftmaxScheduleParams &s) {
     __shared__ int warp_sums[SCHED_THREADS / 32];
     __shared__ int carry_sh;
     const int tid = threadIdx.x;
-    pdl_wait();    // before the kernel behind may start: it reads what came before this one
-    pdl_launch();
     int bad = 0;
     if (tid == 0 && (s.cu[0] != 0 || s.cu[s.nseq] != s.T)) bad = 1;
     for (int i = tid; i < s.nseq; i += SCHED_THREADS)
@@ -1080,6 +1078,12 @@ __global__ void __launch_bounds__(SCHED_THREADS, 1) la_softmax_schedule_kernel(c
         s.hdr[HDR_G] = ne;
         s.hdr[HDR_TOTAL] = ne * s.items_per_entry;
     }
+}
+
+__global__ void __launch_bounds__(SCHED_THREADS, 1) la_softmax_schedule_kernel(const SoftmaxScheduleParams s) {
+    pdl_wait();    // before the kernel behind may start: it reads what came before this one
+    pdl_launch();
+    softmax_schedule(s);
 }
 
 }  // namespace la

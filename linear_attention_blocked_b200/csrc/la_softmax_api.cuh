@@ -25,9 +25,13 @@ SoftmaxLayout softmax_layout(int nseq, long long T) {
 }
 
 // Work items of the prompt kernel: pairs of query tiles.  With no more items
-// than SMs every CTA has one at most, which it finds itself: no scheduler launch
+// than SMs every CTA has one, which it finds itself: no scheduler launch
 // and no workspace (129 tokens, 64 heads over 8: 14.4 us with, 12.3 us without; back
-// to back, with the next call set up meanwhile, 10.2 us).
+// to back, with the next call set up meanwhile, 10.2 us).  The count is a bound, half
+// an entry per sequence too high on average: where the likely count fits and items
+// are short, those too many wait for an SM (9 sequences of up to 500, 8 heads over 8,
+// at most 152 items: 19.2 us with the scheduler, 15.9 us without; a second wave
+// that really comes costs more: 700 tokens, 64 heads over 8, 192 items, 22.2 / 25.2).
 // Depends on the shape only, so that the workspace size does.
 struct SoftmaxItems {
     int rows, pairs;   // rows per entry, pairs per entry and key/value head
@@ -52,8 +56,9 @@ SoftmaxItems softmax_items(int nseq, long long T, long long keys, int H, int Hkv
     SoftmaxItems s;
     s.rows = G % 2 ? 2 * la::BLK : la::BLK;
     s.pairs = G % 2 ? G : G / 2;
-    s.items = (T / s.rows + nseq) * Hkv * s.pairs;
-    s.direct = T > 0 && s.items <= 148;
+    const long long per = (long long)Hkv * s.pairs;
+    s.items = (T + (long long)nseq * (s.rows - 1)) / s.rows * per;
+    s.direct = T > 0 && (s.items <= 148 || (keys <= 1024 && s.items - (nseq - 1) * per / 2 <= 148));
     s.split = s.direct && s.items <= 96 && keys > 13 * la::BLK;
     return s;
 }
@@ -627,9 +632,6 @@ la_status la_softmax_prefill_backward_varlen(const void *q, const void *k, const
     sp.prefix = reinterpret_cast<int *>(ws + w.tables.prefix);
     sp.entries = reinterpret_cast<int4 *>(ws + w.tables.entries);
     sp.status = status;
-    if (!launch_dependent(la::la_softmax_schedule_kernel, dim3(1), la::SCHED_THREADS, 0, stream, sp)) return LA_ERR_CUDA;
-    ++g_launches;
-    if (T == 0) return LA_OK;
 
     la::SoftmaxBwdParams bp;
     float *lse2 = reinterpret_cast<float *>(ws + w.lse2), *delta = reinterpret_cast<float *>(ws + w.delta);
@@ -652,17 +654,18 @@ la_status la_softmax_prefill_backward_varlen(const void *q, const void *k, const
     bp.wait_limit_ns = g_wait_limit_ns.load();
     bp.status = status;
 
+    const long long row_blocks = (T * H + la::SCHED_THREADS / 16 - 1) / (la::SCHED_THREADS / 16);
+    if (!launch_dependent(la::la_softmax_rows_kernel, dim3(1 + (unsigned)(row_blocks < 148 * 4 ? row_blocks : 148 * 4)),
+                          la::SCHED_THREADS, 0, stream, sp, static_cast<const __nv_bfloat16 *>(out),
+                          static_cast<const __nv_bfloat16 *>(dout), lse, lse2, delta, (int)T, H))
+        return LA_ERR_CUDA;
+    ++g_launches;
+    if (T == 0) return LA_OK;  // (the tables are checked)
+
     CUtensorMap mq, mk, mv, mg;
     if (!encode_qkv_map(&mq, q, (int)T, H) || !encode_qkv_map(&mk, k, (int)T, Hkv) ||
         !encode_qkv_map(&mv, v, (int)T, Hkv) || !encode_qkv_map(&mg, dout, (int)T, H))
         return LA_ERR_CUDA;
-    const long long row_blocks = (T * H + la::SB_ROWS_THREADS / 16 - 1) / (la::SB_ROWS_THREADS / 16);
-    if (!launch_dependent(la::la_softmax_rows_kernel, dim3((unsigned)(row_blocks < 148 * 16 ? row_blocks : 148 * 16)),
-                          la::SB_ROWS_THREADS, 0, stream, static_cast<const __nv_bfloat16 *>(out),
-                          static_cast<const __nv_bfloat16 *>(dout), lse, lse2, delta, (int)T, H))
-        return LA_ERR_CUDA;
-    ++g_launches;
-
     if ((st = ensure_smem_attr(g_attr_softmax_dkv, la::la_softmax_dkv_kernel, la::DKV_SMEM)) != LA_OK) return st;
     if ((st = ensure_smem_attr(g_attr_softmax_dq, la::la_softmax_dq_kernel, la::DQ_SMEM)) != LA_OK) return st;
     const int sms = device_sm_count();

@@ -66,33 +66,37 @@ __device__ __forceinline__ void store_row32(__nv_bfloat16 *to, uint32_t (&o)[32]
 }
 
 // delta_t = g_t . o_t and lse_t log2 e, both as [H, T]: 16 lanes per (token, head).
-constexpr int SB_ROWS_THREADS = 256;
-__global__ void __launch_bounds__(SB_ROWS_THREADS)
-la_softmax_rows_kernel(const __nv_bfloat16 *out, const __nv_bfloat16 *dout, const float *lse, float *lse2,
-                       float *delta, int T, int H) {
-    pdl_launch();  // (the kernel behind waits for this one's end before it reads the rows)
+// The first block is the scheduler, beside the others: a launch less.
+__global__ void __launch_bounds__(SCHED_THREADS, 2)
+la_softmax_rows_kernel(const SoftmaxScheduleParams s, const __nv_bfloat16 *out, const __nv_bfloat16 *dout,
+                       const float *lse, float *lse2, float *delta, int T, int H) {
+    pdl_wait();    // before the kernel behind may start: it reads what came before this one
+    pdl_launch();
+    if (blockIdx.x == 0) {
+        softmax_schedule(s);
+        return;
+    }
     const long long total = (long long)T * H;
     const int l16 = threadIdx.x & 15;
-    for (long long e = ((long long)blockIdx.x * SB_ROWS_THREADS + threadIdx.x) >> 4; e < total;
-         e += ((long long)gridDim.x * SB_ROWS_THREADS) >> 4) {
+    for (long long e = ((long long)(blockIdx.x - 1) * SCHED_THREADS + threadIdx.x) >> 4; e < total;
+         e += ((long long)(gridDim.x - 1) * SCHED_THREADS) >> 4) {
         const uint4 a = reinterpret_cast<const uint4 *>(out + e * D)[l16];
         const uint4 b = reinterpret_cast<const uint4 *>(dout + e * D)[l16];
         const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-        float s = 0.f;
+        float x = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            s = fmaf(__uint_as_float(av[i] << 16), __uint_as_float(bv[i] << 16), s);
-            s = fmaf(__uint_as_float(av[i] & 0xffff0000u), __uint_as_float(bv[i] & 0xffff0000u), s);
+            x = fmaf(__uint_as_float(av[i] << 16), __uint_as_float(bv[i] << 16), x);
+            x = fmaf(__uint_as_float(av[i] & 0xffff0000u), __uint_as_float(bv[i] & 0xffff0000u), x);
         }
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o, 16);
+        for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o, 16);
         if (l16 == 0) {
             const long long t = e / H, h = e - t * H;
-            delta[h * T + t] = s;
+            delta[h * T + t] = x;
             lse2[h * T + t] = lse[e] * 1.44269504088896341f;
         }
     }
-    pdl_wait();  // the scheduler has ended when this kernel has
 }
 
 // ---------------------------------------------------------------------------
