@@ -793,7 +793,8 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
                         }
                     }
                 }
-                const f32x2 c2 = pack2(c, c), mc2 = pack2(-m * c, -m * c);
+                const float mc = m == -INFINITY ? 0.f : -m * c;  // (only scores of -inf so far: no weight)
+                const f32x2 c2 = pack2(c, c), mc2 = pack2(mc, mc);
                 f32x2 s2[2] = {0ull, 0ull};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {  // 32 columns at a time: 16 TMEM columns of bf16 pairs

@@ -143,3 +143,33 @@ def test_calls_at_once_on_two_streams():
             for a, b in zip(x, y):
                 assert torch.equal(a, b)
     assert la.get_device_status() == la.LA_OK
+
+
+def test_keys_whose_scores_are_all_minus_infinity():
+    """The first keys of a row, more than a tile of them, score -inf: they have no
+    weight, and the row is that of the keys behind them.  A row with no others has
+    no result."""
+    def lower(q, k, first):
+        q[..., 0] = q[..., 0].abs() + 0.5
+        k[:first, :, 0] = float("-inf")
+
+    for lens, first, heads in (([400], 130, (8, 2)), ([3001], 1500, (2, 1))):
+        q, k, v, _, cu = packed(lens, *heads, 21)
+        lower(q, k, first)
+        out, lse = la.softmax_prefill_varlen(q, k, v, cu, lens[0])
+        check(out[first:], lse[first:], attention64(q[first:], k[first:], v[first:], 0, S), lens[0])
+        assert torch.isnan(out[:first]).all() and (lse[:first] == float("-inf")).all()
+    for new, past, first in ((20, 700, 300), (20, 5000, 4000)):
+        c = Cache([past], [new + 1], 1, 32, 22)
+        q, k, v, _, cu = packed([new], 8, 1, 23)
+        lower(q, c.past[0][0], first)
+        c.write(0, 0, *c.past[0])
+        out, lse = la.softmax_prefill_paged(q, k, v, cu, new, c.k, c.v, c.table, c.lens)
+        kk, vv = c.read(0, past + new)
+        check(out, lse, attention64(q, kk[first:], vv[first:], past - first, S), past + new)
+        c.lens += new
+        dec, dlse = la.softmax_decode_paged(q[:1], k[:1], v[:1], c.k, c.v, c.table, c.lens)
+        kk, vv = c.read(0, past + new + 1)
+        check(dec, dlse, attention64(q[:1], kk[first:], vv[first:], past + new - first, S), past + new + 1,
+              p_step=2.0 ** -16)
+    assert la.get_device_status() == la.LA_OK
