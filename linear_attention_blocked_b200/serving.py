@@ -132,8 +132,10 @@ class PagePool:
         for i in shared:
             page = self._take()
             if i * self.page_size < n:                    # it holds tokens: the ragged page
-                self._copies.append((pages[i], page))
-                self._held.update((pages[i], page))
+                # (a page that a collected copy is still to fill: that copy's source)
+                src = next((s for s, d in self._copies if d == pages[i]), pages[i])
+                self._copies.append((src, page))
+                self._held.update((src, page))
             self._drop(pages[i])
             pages[i] = page
         while len(pages) < last:

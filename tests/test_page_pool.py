@@ -138,3 +138,24 @@ def test_tables_and_refusals():
         pool.compact()
     pool.take_copies()
     pool.compact()
+
+
+def test_fork_of_a_fork_before_its_copy_is_taken():
+    """A page that a collected copy will fill is forked again: the second copy
+    reads what the first one reads, and no page is both source and destination."""
+    pool = PagePool(8, 16)
+    a = pool.add()
+    pool.reserve(a, 20)
+    pool.advance(a, 20)
+    b = pool.fork(a)
+    pool.reserve(b, 1)
+    c = pool.fork(b)
+    pool.reserve(c, 1)
+    d = pool.fork(c)
+    pool.reserve(d, 30)
+    src, dst = pool.take_copies()
+    assert not set(src) & set(dst) and len(set(dst)) == len(dst)
+    held = dict(zip(dst.tolist(), src.tolist()))
+    for r in (b, c, d):
+        assert held[pool.pages(r)[1]] == pool.pages(a)[1]
+    assert len({pool.pages(r)[1] for r in (a, b, c, d)}) == 4
