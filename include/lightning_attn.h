@@ -436,7 +436,9 @@ LA_API la_status la_softmax_prefill_varlen(const void *q, const void *k, const v
  *   dk_s  = scale sum_t dS_ts q_t,   dv_s = sum_t P_ts dout_t
  *
  * dk and dv are summed over the query heads of their group, in fp32 and in a
- * fixed order (no atomics).  out and lse are those of the forward call.  dout,
+ * fixed order (no atomics).  out and lse are those of the forward call.  The
+ * first 128 rows of a sequence take delta as sum_s P_ts dout_t . v_s, which the
+ * rounding of out to bf16 does not touch.  dout,
  * dq: bf16 [total_tokens, H, d]; dk, dv: bf16 [total_tokens, Hkv, d]; the four
  * and the workspace (la_softmax_prefill_backward_varlen_workspace_size bytes,
  * 256-byte aligned) must not overlap the inputs or each other.  The gradient of

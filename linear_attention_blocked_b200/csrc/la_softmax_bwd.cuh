@@ -19,6 +19,13 @@
 // that sum over them take them as their first operand: shared memory holds
 // only what TMA brought.
 //
+// delta_t = g_t . o_t is off by the rounding of o to bf16.  In a row of few keys, or
+// of one heavy key, g_t . v_s - delta_t may be much smaller than either, so the first
+// 128 rows of a sequence, which meet all their keys in one step, take
+// delta_t = sum_s P_ts (g_t . v_s) from that step, in fp32: with sequences of 2 tokens
+// dq is off by 0.0023 of its norm instead of 0.0037 (dS and the result, rounded to
+// bf16, alone make 0.0023).  8 sequences of 60, 64 heads over 8: 43.5 us, 39.8 without.
+//
 // 8192 tokens, 16 heads over 2: dk and dv 424 us, 1297 TFLOP/s, tensor pipe busy
 // 64 %; dq 277 us, 1488 TFLOP/s, 74 %.  What is left is the way from a product
 // through TMEM, the exponentials or the sums and back to the next product.
@@ -119,7 +126,8 @@ la_softmax_rows_kernel(const SoftmaxScheduleParams s, const __nv_bfloat16 *out, 
 constexpr int DKV_K = 0, DKV_V = TILE_BYTES, DKV_RING = 2 * TILE_BYTES;  // ring: 2 x (Q, g)
 constexpr int DKV_ROWS = DKV_RING + 4 * TILE_BYTES;                      // 2 x (lse2 [128], delta [128])
 constexpr int DKV_CTRL = DKV_ROWS + 2 * 2 * BLK * 4;
-constexpr int DKV_SMEM = DKV_CTRL + 512;
+constexpr int DKV_SUMS = DKV_CTRL + 512;                                 // [2][4 warps][64 columns]
+constexpr int DKV_SMEM = DKV_SUMS + 2 * 4 * 64 * 4;
 constexpr int SB_SLOTS = 4;
 
 struct DkvCtrl {
@@ -128,6 +136,7 @@ struct DkvCtrl {
     uint64_t kv_full, kv_empty;           // [1], [1]
     uint64_t s_full, p_full;              // [1], [8]
     uint64_t dp_full, ds_full;            // [1], [8]
+    uint64_t sum_full[2];                 // [4] a warpgroup's exact delta: sums of its warps, then joined
     uint64_t acc_full;                    // [1] an item's dv and dk are complete
     uint64_t item_full[SB_SLOTS], item_empty[SB_SLOTS];  // [1], [11]
     uint64_t fin;
@@ -184,6 +193,8 @@ la_softmax_dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_cons
         mbar_init(&cb->p_full, 8);
         mbar_init(&cb->dp_full, 1);
         mbar_init(&cb->ds_full, 8);
+        mbar_init(&cb->sum_full[0], 4);
+        mbar_init(&cb->sum_full[1], 4);
         mbar_init(&cb->acc_full, 1);
         for (int s = 0; s < SB_SLOTS; ++s) {
             mbar_init(&cb->item_full[s], 1);
@@ -447,6 +458,37 @@ la_softmax_dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_cons
                     if (!wait(&cb->dp_full, n & 1)) { ok = false; break; }
                     tc_fence_after();
                     tmem_ld_cols<64>(tdp, x);
+                    if (i == 0) {  // a sequence's first rows: delta from this step, into its place among the rows
+                        float *sums = reinterpret_cast<float *>(smem + DKV_SUMS) + wg * 4 * 64;
+                        const int lim = r < im[BI_LEN] ? r - wg * 64 : 64;  // (a key behind the end may hold anything)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            float v[32];
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                v[k] = half * 32 + k < lim ? 0.f : pr[half * 32 + k] * __uint_as_float(x[half * 32 + k]);
+                            // over the warp's keys: lane l ends with column half * 32 + l
+#pragma unroll
+                            for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                                for (int k = 0; k < o; ++k) {
+                                    const float keep = lane & o ? v[k + o] : v[k], send = lane & o ? v[k] : v[k + o];
+                                    v[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                                }
+                            sums[(warp & 3) * 64 + half * 32 + lane] = v[0];
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&cb->sum_full[wg]);
+                        if (!wait(&cb->sum_full[wg], 0)) { ok = false; break; }
+                        if ((warp & 3) < 2) {
+                            const int q = (warp & 3) * 32 + lane;
+                            reinterpret_cast<float *>(smem + DKV_ROWS)[s * 2 * BLK + BLK + wg * 64 + q] =
+                                (sums[q] + sums[64 + q]) + (sums[128 + q] + sums[192 + q]);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&cb->sum_full[wg]);
+                        if (!wait(&cb->sum_full[wg], 1)) { ok = false; break; }
+                    }
 #pragma unroll
                     for (int q = 0; q < 16; ++q) {
                         const float4 de = rows[32 + q];
@@ -530,13 +572,16 @@ __global__ void __launch_bounds__(256) la_softmax_dkv_sum_kernel(const int *hdr,
 constexpr int DQ_STAGES = 5;
 constexpr int DQ_Q = 0, DQ_G = TILE_BYTES, DQ_RING = 2 * TILE_BYTES;
 constexpr int DQ_CTRL = DQ_RING + DQ_STAGES * TILE_BYTES;
-constexpr int DQ_SMEM = DQ_CTRL + 512;
+constexpr int DQ_SUMS = DQ_CTRL + 512;               // [2][128] rows
+constexpr int DQ_SMEM = DQ_SUMS + 2 * BLK * 4;
+static_assert(DKV_SMEM <= 227 * 1024 && DQ_SMEM <= 227 * 1024, "shared memory of one CTA");
 
 struct DqCtrl {
     uint64_t kv_full[DQ_STAGES], kv_empty[DQ_STAGES];
     uint64_t q_full, q_empty;             // [1], [1]
     uint64_t s_full[2];                   // [1]
     uint64_t dp_full, ds_full;            // [1], [8]
+    uint64_t sum_full;                    // [8] the halves of exact deltas
     uint64_t acc_full;                    // [1]
     uint64_t item_full[SB_SLOTS], item_empty[SB_SLOTS];  // [1], [10]
     uint64_t fin;
@@ -569,6 +614,7 @@ la_softmax_dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         mbar_init(&cb->s_full[1], 1);
         mbar_init(&cb->dp_full, 1);
         mbar_init(&cb->ds_full, 8);
+        mbar_init(&cb->sum_full, 8);
         mbar_init(&cb->acc_full, 1);
         for (int s = 0; s < SB_SLOTS; ++s) {
             mbar_init(&cb->item_full[s], 1);
@@ -746,14 +792,15 @@ la_softmax_dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         const uint32_t trow = (uint32_t)(warp & 3) << 21;
         const uint32_t tdp = TDP + trow + wg * 64;
         const float c = p.scale_log2;
-        uint32_t it = 0, n = 0, items = 0;
+        uint32_t it = 0, n = 0, items = 0, firsts = 0;
         int im[BI_FIELDS];
         bool ok = true;
         while (ok && next(it, im)) {
             const int h = im[BI_KVH] * p.G + im[BI_G0], row = im[BI_BLK] * BLK + r;
             const bool mine = row < im[BI_LEN];
             const size_t st = (size_t)h * p.T + im[BI_TOK0] + row;
-            const float ls = mine ? p.lse2[st] : 0.f, de = mine ? p.delta[st] : 0.f;
+            const float ls = mine ? p.lse2[st] : 0.f;
+            float de = mine ? p.delta[st] : 0.f;
             const int ns = im[BI_BLK] + 1;
             for (int j = 0; j < ns; ++j, ++n) {
                 // each S buffer's phase advances once per two steps
@@ -767,6 +814,21 @@ la_softmax_dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                 if (!wait(&cb->dp_full, n & 1)) { ok = false; break; }
                 tc_fence_after();
                 tmem_ld_cols<64>(tdp, x);
+                if (ns == 1) {  // a sequence's first rows: delta from this step
+                    float *sums = reinterpret_cast<float *>(smem + DQ_SUMS);
+                    const int lim = r - wg * 64;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int q = 0; q < 64; ++q)
+                        if (q <= lim) sum = fmaf(pr[q], __uint_as_float(x[q]), sum);
+                    // (read by both warpgroups before ds_full, and so before the next item's)
+                    sums[wg * BLK + r] = sum;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&cb->sum_full);
+                    if (!wait(&cb->sum_full, firsts & 1)) { ok = false; break; }
+                    ++firsts;
+                    de = sums[r] + sums[BLK + r];
+                }
 #pragma unroll
                 for (int q = 0; q < 64; ++q) pr[q] *= __uint_as_float(x[q]) - de;
                 if (j == ns - 1) {  // the diagonal; what it hides may hold anything

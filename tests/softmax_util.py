@@ -108,7 +108,7 @@ class Cache:
         return self.k[pid, :, off], self.v[pid, :, off]
 
 
-def gradients64(q, k, v, g, scale):
+def gradients64(q, k, v, g, scale, own_delta=False):
     """Gradients of one sequence (no past) for dL/dout = g, and bounds of what
     the kernels' roundings may add to them: {"q": (dq, bound), ...}.
 
@@ -116,7 +116,10 @@ def gradients64(q, k, v, g, scale):
     once: half a step of 2^-8 each.  delta = g . out is formed from the bf16
     out, which `check` allows to be off by 2^-8 (|out| + A) + f A.  fp32: P is
     off by a factor of 1 +- r, r = 4 e + 2^-21 + smax 2^-22 as in `check`;
-    g . v and delta are sums of 128 terms; sums over n terms add n 2^-23."""
+    g . v and delta are sums of 128 terms; sums over n terms add n 2^-23.
+
+    own_delta (sequences of at most 128 tokens): delta is the fp32 sum of P (g . v),
+    off by the errors of its P and g . v and of a sum over n terms."""
     n, H, _ = q.shape
     Hkv = k.shape[1]
     G = H // Hkv
@@ -136,6 +139,9 @@ def gradients64(q, k, v, g, scale):
         o_off = BF16 * o.abs() + A[:, h] * (BF16 + r) * (1 + BF16)
         off = (g64.abs() * o_off).sum(1, keepdim=True) + 129 * u * (g64.abs() @ v64.abs().T +
                                                                      (g64 * o).abs().sum(1, keepdim=True))
+        if own_delta:
+            dp_off = 129 * u * (g64.abs() @ v64.abs().T)
+            off = dp_off + (p * (dp.abs() * (r + n * 2 * u) + dp_off)).sum(1, keepdim=True)
         ds_off = ds.abs() * (BF16 + 2 * r) + p * off * (1 + BF16) * (1 + r)
         p_off = p * (BF16 + 2 * r)
         dq[:, h] = ds @ k64 * scale

@@ -139,3 +139,23 @@ def test_gradients_of_a_shared_head_in_parts():
     in parts by several CTAs."""
     run_and_check([300, 1, 129], 24, 1, seed=29)
     run_and_check([1300], 64, 1, seed=31)
+
+
+@pytest.mark.parametrize("scale", [1.5, 8.0])
+@pytest.mark.parametrize("heads", [(8, 8), (8, 2), (3, 1)], ids=str)
+def test_short_sequences_take_no_error_from_the_rounded_output(heads, scale):
+    """Rows of few keys, or of one heavy key, whose gradients are small against the
+    terms that they are differences of: bounds without the rounding of `out`."""
+    lens = [2] * 20 + [1, 3, 0, 5, 128, 2, 127, 64, 31]
+    q, k, v, cu, cu_dev = packed(lens, *heads, seed=heads[0], scale=scale)
+    g = torch.randn_like(q)
+    out, lse = la.softmax_prefill_varlen(q, k, v, cu_dev, max(lens))
+    got = la.softmax_prefill_backward_varlen(q, k, v, out, lse, g, cu_dev, max(lens))
+    assert la.get_device_status() == la.LA_OK
+    for a, b in zip(cu[:-1], cu[1:]):
+        if a == b:
+            continue
+        want = gradients64(q[a:b], k[a:b], v[a:b], g[a:b], 128 ** -0.5, own_delta=True)
+        for x, (name, (y, bound)) in zip(got, want.items()):
+            over = ((x[a:b].double() - y).abs() / bound).max().item()
+            assert over <= 1, f"d{name} of {b - a} tokens off by {over:.2f} of its bound"
