@@ -178,6 +178,26 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+// One thread's row of 32 fp32 TMEM columns, times f, as bf16.  Whole sectors where
+// the tensor's address allows it (wide: 32-byte aligned; rows are then, too): in
+// 16-byte stores 48 prompts of 512 tokens, 64 heads over 8, take 416 us instead of
+// 396, 12 of up to 4059 1396 instead of 1367.
+__device__ __forceinline__ bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
+__device__ __forceinline__ void store_row32(__nv_bfloat16 *to, uint32_t (&o)[32], float f, bool wide) {
+    scale32(o, f);
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+    if (wide) {
+        st_global_v8(to, w);
+        st_global_v8(to + 16, w + 8);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4 *>(to)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+}
+
 // Bounded waits of a control block with `abort`: as wait_or_abort above.
 template <class Ctrl>
 __device__ __forceinline__ bool ctrl_wait(uint64_t *bar, uint32_t parity, unsigned long long limit_ns, int *status,
@@ -843,6 +863,7 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
         uint32_t it = 0, n[2] = {0, 0};
         int im[SI_FIELDS];
         bool ok = true;
+        const bool wide = aligned32(p.out);
         constexpr uint32_t MASK = ~(1u << SI_PAST | 1u << SI_KVH | 1u << SI_SEQ);
         while (ok && smx_next<MASK>(it, im, lane, p, cb)) {
 #pragma unroll
@@ -877,16 +898,7 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
                             reinterpret_cast<uint4 *>(part + q * 32)[i] =
                                 make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     } else if (mine) {
-                        uint4 *to = reinterpret_cast<uint4 *>(p.out + at * D + q * 32);
-                        scale32(o, inv);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                w[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]), __uint_as_float(o[8 * i + 2 * k + 1]));
-                            to[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
+                        store_row32(p.out + at * D + q * 32, o, inv, wide);
                     }
                 }
                 tc_fence_before();

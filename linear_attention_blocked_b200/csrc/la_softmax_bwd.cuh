@@ -63,19 +63,6 @@ __device__ __forceinline__ void tmem_st_bf16x64(uint32_t taddr, const float (&x)
 // warpgroups, each inside its own half of the fp32 tile that it replaces
 __device__ __forceinline__ uint32_t half_cols(int kk) { return (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8); }
 
-// One thread's row of 32 fp32 TMEM columns, times f, as bf16
-__device__ __forceinline__ void store_row32(__nv_bfloat16 *to, uint32_t (&o)[32], float f) {
-    scale32(o, f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            w[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]), __uint_as_float(o[8 * i + 2 * k + 1]));
-        reinterpret_cast<uint4 *>(to)[i] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-}
-
 // delta_t = g_t . o_t and lse_t log2 e, both as [H, T]: 16 lanes per (token, head).
 // The first block is the scheduler, beside the others: a launch less (1 to 2 us).
 __global__ void __launch_bounds__(SCHED_THREADS, 2)
@@ -422,6 +409,7 @@ la_softmax_dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_cons
         const uint32_t trow = (uint32_t)(warp & 3) << 21;
         const uint32_t ts = TS + trow + wg * 64, tdp = TDP + trow + wg * 64;
         const float c = p.scale_log2;
+        const bool wide = aligned32(wg ? p.dk : p.dv);
         uint32_t it = 0, n = 0, items = 0;
         int im[BI_FIELDS];
         bool ok = true;
@@ -522,10 +510,9 @@ la_softmax_dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_cons
                     scale32(o, f);
                     float *to = p.parts + ((size_t)im[BI_PART] * 2 + wg) * p.T * p.Hkv * D + at + q * 32;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        reinterpret_cast<uint4 *>(to)[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    for (int k = 0; k < 4; ++k) st_global_v8(to + 8 * k, o + 8 * k);  // (the workspace is 256-byte aligned)
                 } else if (mine) {
-                    store_row32((wg ? p.dk : p.dv) + at + q * 32, o, f);
+                    store_row32((wg ? p.dk : p.dv) + at + q * 32, o, f, wide);
                 }
             }
             tc_fence_before();
@@ -792,6 +779,7 @@ la_softmax_dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
         const uint32_t trow = (uint32_t)(warp & 3) << 21;
         const uint32_t tdp = TDP + trow + wg * 64;
         const float c = p.scale_log2;
+        const bool wide = aligned32(p.dq);
         uint32_t it = 0, n = 0, items = 0, firsts = 0;
         int im[BI_FIELDS];
         bool ok = true;
@@ -853,7 +841,7 @@ la_softmax_dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                 uint32_t o[32];
                 __syncwarp();
                 tmem_ld_wait32(TDQ + trow + wg * 64 + q * 32, o);
-                if (mine) store_row32(to + q * 32, o, p.scale);
+                if (mine) store_row32(to + q * 32, o, p.scale, wide);
             }
             tc_fence_before();
             __syncwarp();

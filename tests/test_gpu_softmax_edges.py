@@ -173,3 +173,23 @@ def test_keys_whose_scores_are_all_minus_infinity():
         check(dec, dlse, attention64(q[:1], kk[first:], vv[first:], past + new - first, S), past + new + 1,
               p_step=2.0 ** -16)
     assert la.get_device_status() == la.LA_OK
+
+
+def test_tensors_aligned_to_16_bytes_only():
+    """Every tensor 16 bytes behind a 32-byte boundary: the same bits."""
+    def shifted(x):
+        buf = torch.empty(x.numel() + 8, dtype=x.dtype, device="cuda")
+        return buf[8:].view(x.shape).copy_(x)
+
+    q, k, v, _, cu = packed([300, 5, 0, 129], 6, 2, 31)
+    g = torch.randn_like(q)
+    out, lse = la.softmax_prefill_varlen(q, k, v, cu, 300)
+    want = la.softmax_prefill_backward_varlen(q, k, v, out, lse, g, cu, 300)
+    q2, k2, v2, g2 = (shifted(x) for x in (q, k, v, g))
+    out2, _ = la.softmax_prefill_varlen(q2, k2, v2, cu, 300, out=shifted(torch.zeros_like(q)), lse=torch.empty_like(lse))
+    got = la.softmax_prefill_backward_varlen(q2, k2, v2, out2, lse, g2, cu, 300, dq=shifted(torch.zeros_like(q)),
+                                             dk=shifted(torch.zeros_like(k)), dv=shifted(torch.zeros_like(v)))
+    assert la.get_device_status() == la.LA_OK
+    assert all(x.data_ptr() % 32 == 16 for x in (out2, *got))
+    for x, y in zip((out2, *got), (out, *want)):
+        assert torch.equal(x, y)
