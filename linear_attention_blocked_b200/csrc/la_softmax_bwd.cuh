@@ -24,7 +24,7 @@
 // 128 rows of a sequence, which meet all their keys in one step, take
 // delta_t = sum_s P_ts (g_t . v_s) from that step, in fp32: with sequences of 2 tokens
 // dq is off by 0.0023 of its norm instead of 0.0037 (dS and the result, rounded to
-// bf16, alone make 0.0023).  8 sequences of 60, 64 heads over 8: 43.5 us, 39.8 without.
+// bf16, alone make 0.0023).  8 sequences of 60, 64 heads over 8: 3.7 us more.
 //
 // 8192 tokens, 16 heads over 2: dk and dv 424 us, 1297 TFLOP/s, tensor pipe busy
 // 64 %; dq 277 us, 1488 TFLOP/s, 74 %.  What is left is the way from a product
