@@ -74,12 +74,17 @@ la_softmax_rows_kernel(const SoftmaxScheduleParams s, const __nv_bfloat16 *out, 
         softmax_schedule(s);
         return;
     }
-    const long long total = (long long)T * H;
-    const int l16 = threadIdx.x & 15;
-    for (long long e = ((long long)(blockIdx.x - 1) * SCHED_THREADS + threadIdx.x) >> 4; e < total;
-         e += ((long long)(gridDim.x - 1) * SCHED_THREADS) >> 4) {
-        const uint4 a = reinterpret_cast<const uint4 *>(out + e * D)[l16];
-        const uint4 b = reinterpret_cast<const uint4 *>(dout + e * D)[l16];
+    const long long total = (long long)T * H, step = ((long long)(gridDim.x - 1) * SCHED_THREADS) >> 4;
+    const int l16 = threadIdx.x & 15, half = (threadIdx.x >> 4) & 1;
+    // A warp has two rows; both halves stay in the loop as long as one has a row, since
+    // the sums' shuffles name all 32 lanes (with odd T H the last warp has one row).
+    for (long long first = ((long long)(blockIdx.x - 1) * SCHED_THREADS + (threadIdx.x & ~31u)) >> 4; first < total;
+         first += step) {
+        const long long e = first + half;
+        const bool has = e < total;
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        const uint4 a = has ? reinterpret_cast<const uint4 *>(out + e * D)[l16] : none;
+        const uint4 b = has ? reinterpret_cast<const uint4 *>(dout + e * D)[l16] : none;
         const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
         float x = 0.f;
 #pragma unroll
@@ -89,7 +94,7 @@ la_softmax_rows_kernel(const SoftmaxScheduleParams s, const __nv_bfloat16 *out, 
         }
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o, 16);
-        if (l16 == 0) {
+        if (has && l16 == 0) {
             const long long t = e / H, h = e - t * H;
             delta[h * T + t] = x;
             lse2[h * T + t] = lse[e] * 1.44269504088896341f;
