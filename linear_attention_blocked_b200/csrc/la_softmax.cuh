@@ -520,6 +520,9 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
         return ctrl_warp_wait(bar, parity, p.wait_limit_ns, p.status, cb);
     };
+    // Every warp: what came before has ended.  The waits below have a limit, which must
+    // not run while the kernel in front still does.
+    pdl_wait();
 
     if (warp < 4) {
         reg_dec<48>();
@@ -529,7 +532,6 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
             int total = 0, ne = 0;
             int4 own = make_int4(0, 0, 0, 0);
             SplitCursor run;
-            pdl_wait();    // what came before has ended: inputs and, when not direct, tables
             pdl_launch();  // the kernel behind may be set up (it waits for this one's end)
             if (p.split) {
                 if (lane == 0) p.info[3 * blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -754,7 +756,6 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
             // ===================== new tokens into their pages =====================
             // (no CTA reads them there: their tiles come from the packed tensors)
             int4 unused;
-            pdl_wait();
             if (smx_find(-1, lane, p, unused) > 0) {
                 const AppendTables at = {p.new_k, p.new_v, p.kc, p.vc, p.cu, p.pages, p.past, p.nseq,
                                          p.Hkv, p.max_pages, p.n_pages, p.page, p.page_shift, p.status};

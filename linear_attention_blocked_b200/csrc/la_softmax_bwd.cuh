@@ -215,13 +215,13 @@ la_softmax_dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_cons
     auto next = [&](uint32_t &it, int (&item)[BI_FIELDS]) -> bool {
         return sb_next(it, item, lane, p.wait_limit_ns, p.status, cb);
     };
+    pdl_wait();  // every warp, before its first wait with a limit: the tables and rows are written
 
     if (warp < 4) {
         reg_dec<72>();
         if (warp == 0) {
             // ===================== items, Q and g tiles =====================
             const uint64_t pol = policy_evict_last();
-            pdl_wait();    // the tables and rows
             pdl_launch();  // dq, which needs nothing of this kernel, fills the SMs that run out of items
             const int ne = p.hdr[HDR_G];
             const long long total = (long long)ne * p.Hkv * p.nparts;
@@ -369,7 +369,6 @@ la_softmax_dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_cons
             // ===================== rows of the steps =====================
             // A query row behind the sequence's end: lse2 = +inf makes its P zero, and
             // its Q and g rows (another sequence's) are zeroed.
-            pdl_wait();
             uint32_t it = 0, n = 0;
             int im[BI_FIELDS];
             bool ok = true;

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import linear_attention_blocked_b200 as la
-from softmax_util import gradients64, packed
+from softmax_util import Cache, gradients64, packed
 
 pytestmark = pytest.mark.gpu
 S = 128 ** -0.5
@@ -29,3 +29,54 @@ def test_odd_numbers_of_rows(lens, heads):
         for x, (name, (want, bound)) in zip(got, gradients64(q[a:b], k[a:b], v[a:b], g[a:b], S).items()):
             over = ((x[a:b].double() - want).abs() / bound).max().item()
             assert over <= 1, f"d{name} of tokens {a}-{b} off by {over:.2f} of its bound"
+
+
+def long_call():
+    """A call of some 5 ms on 100 of the SMs: one new token of 200 heads behind 400000
+    cached ones that they share.  The SMs left over take the next kernel's CTAs at once."""
+    past, page = 400000, 128
+    pages = past // page + 1
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    kc, vc = (torch.randn(pages, 1, page, 128, generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    q, k, v, _, cu = packed([1], 200, 1, 4)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([past], dtype=torch.int32, device="cuda")
+    return lambda: la.softmax_prefill_paged(q, k, v, cu, 1, kc, vc, table, lens)
+
+
+@pytest.mark.parametrize("kind", ["prompt", "runs", "chunk", "gradients"])
+def test_limits_do_not_count_the_kernel_in_front(kind):
+    """A kernel that starts while the one in front of it still runs waits for that one's
+    end before its own time limits begin."""
+    long = long_call()
+    lens = [3000] if kind == "runs" else [60]
+    q, k, v, _, cu = packed(lens, 2, 1, 5)
+    c = Cache([100], [60], 1, 16, 6)
+    g = torch.randn_like(q)
+    o, l = la.softmax_prefill_varlen(q, k, v, cu, lens[0])
+
+    def call():
+        if kind == "chunk":
+            return la.softmax_prefill_paged(q, k, v, cu, 60, c.k, c.v, c.table, c.lens)
+        if kind == "gradients":
+            return la.softmax_prefill_backward_varlen(q, k, v, o, l, g, cu, 60)
+        return la.softmax_prefill_varlen(q, k, v, cu, lens[0])
+    want = call()
+    long()
+    torch.cuda.synchronize()
+    assert la.get_device_status() == la.LA_OK
+    begin, middle, end = (torch.cuda.Event(enable_timing=True) for _ in range(3))
+    begin.record()
+    long()
+    middle.record()
+    torch.cuda.synchronize()
+    assert begin.elapsed_time(middle) > 2.0, "the call in front is too short to show anything"
+    try:
+        long()
+        la.set_wait_limit_ns(1_000_000)
+        got = call()
+    finally:
+        la.set_wait_limit_ns(0)
+    assert la.get_device_status() == la.LA_OK
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
