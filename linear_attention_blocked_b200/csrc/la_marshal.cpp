@@ -8,6 +8,9 @@
 // and the Python code takes it, with its full checks and messages.
 #include <Python.h>
 
+#include <algorithm>
+#include <array>
+
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
@@ -40,17 +43,36 @@ at::Tensor make(at::IntArrayRef sizes, at::ScalarType type, int dev) {
     return at::detail::empty_cuda(sizes, type, at::Device(at::kCUDA, (c10::DeviceIndex)dev), c10::nullopt);
 }
 
-// An output that was passed (and fits) or is made now.
-bool output(PyObject *o, at::Tensor &to, at::IntArrayRef sizes, at::ScalarType type, int dev) {
-    if (o == Py_None) {
-        to = make(sizes, type, dev);
+// An output: one that was passed (and fits), or one to be made, or (not `want`ed) none.
+struct Output {
+    at::Tensor t;
+    std::array<int64_t, 3> sizes;
+    int dim;
+    at::ScalarType type;
+    bool make_it;
+    bool ok(PyObject *o, std::initializer_list<int64_t> s, at::ScalarType ty, int dev, bool want = true) {
+        dim = (int)s.size();
+        std::copy(s.begin(), s.end(), sizes.begin());
+        type = ty;
+        make_it = want && o == Py_None;
+        if (o == Py_None) return true;
+        Arg a;
+        if (!a.ok(o, type, dim, dev) || !a.sized(s)) return false;
+        t = *a.t;
         return true;
     }
-    Arg a;
-    if (!a.ok(o, type, (int)sizes.size(), dev) || !a.t->sizes().equals(sizes)) return false;
-    to = *a.t;
-    return true;
-}
+    void *ptr(int dev) {
+        if (make_it) t = make(at::IntArrayRef(sizes.data(), dim), type, dev);
+        return t.defined() ? t.data_ptr() : nullptr;
+    }
+};
+
+// Other Python threads run meanwhile: an allocation or a launch may block (a full launch
+// queue), and what it waits for may need one of them.
+struct Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
 
 // q [T, H, d], k and v [T, Hkv, d] on the current device
 struct Qkv {
@@ -82,6 +104,24 @@ struct Cache {
         max_pages = (int)table.size(1);
         return k.sized({n_pages, x.Hkv, page, x.d}) && v.sized({n_pages, x.Hkv, page, x.d}) &&
                table.sized({n, max_pages}) && lens.size(0) == n;
+    }
+};
+
+struct CachePtrs {
+    void *k, *v;
+    const int *table, *lens;
+    explicit CachePtrs(const Cache &c)
+        : k(c.k.ptr()), v(c.v.ptr()), table((const int *)c.table.ptr()), lens((const int *)c.lens.ptr()) {}
+};
+
+struct Workspace {
+    size_t bytes;
+    at::Tensor t;
+    void *at = nullptr;
+    Workspace(size_t n, int dev) : bytes(n) {
+        if (!n) return;
+        t = make({(int64_t)n}, at::kByte, dev);
+        at = t.data_ptr();
     }
 };
 
@@ -139,19 +179,21 @@ PyObject *prefill_varlen(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (n != 9 || !x.ok(a) || !cu.ok(a[3], INT32, 1, x.dev) || cu.size(0) < 1 || !small(cu.size(0)) ||
             !number(a[4], longest) || !number(a[5], scale))
             Py_RETURN_NONE;
-        at::Tensor out, lse, ws;
-        if (!output(a[6], out, {x.T, x.H, x.d}, BF16, x.dev)) Py_RETURN_NONE;
+        Output out, lse;
         const int want = truth(a[8]);
-        if (want < 0) Py_RETURN_NONE;
-        if ((a[7] != Py_None || want) && !output(a[7], lse, {x.T, x.H}, FP32, x.dev)) Py_RETURN_NONE;
+        if (want < 0 || !out.ok(a[6], {x.T, x.H, x.d}, BF16, x.dev) || !lse.ok(a[7], {x.T, x.H}, FP32, x.dev, want))
+            Py_RETURN_NONE;
         const int nseq = (int)cu.size(0) - 1;
-        const size_t bytes = la_softmax_prefill_varlen_workspace_size(nseq, x.T, x.H, x.Hkv, x.d);
-        if (bytes) ws = make({(int64_t)bytes}, at::kByte, x.dev);
-        const la_status st = la_softmax_prefill_varlen(
-            x.q.ptr(), x.k.ptr(), x.v.ptr(), (const int *)cu.ptr(), nseq, x.T, longest, x.H, x.Hkv, x.d, scale,
-            out.data_ptr(), lse.defined() ? (float *)lse.data_ptr() : nullptr, bytes ? ws.data_ptr() : nullptr, bytes,
-            stream_of(x.dev));
-        return result(st, out, lse);
+        const void *q = x.q.ptr(), *k = x.k.ptr(), *v = x.v.ptr();
+        const int *seqs = (const int *)cu.ptr();
+        const la_status st = [&] {
+            Unlocked free;
+            void *o = out.ptr(x.dev), *l = lse.ptr(x.dev);
+            Workspace ws(la_softmax_prefill_varlen_workspace_size(nseq, x.T, x.H, x.Hkv, x.d), x.dev);
+            return la_softmax_prefill_varlen(q, k, v, seqs, nseq, x.T, longest, x.H, x.Hkv, x.d, scale, o, (float *)l,
+                                             ws.at, ws.bytes, stream_of(x.dev));
+        }();
+        return result(st, out.t, lse.t);
     });
 }
 
@@ -166,20 +208,23 @@ PyObject *prefill_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (n != 13 || !x.ok(a) || !cu.ok(a[3], INT32, 1, x.dev) || cu.size(0) < 1 || !small(cu.size(0)) ||
             !number(a[4], longest) || !c.ok(a + 5, x, (int)cu.size(0) - 1) || !number(a[9], scale))
             Py_RETURN_NONE;
-        at::Tensor out, lse, ws;
-        if (!output(a[10], out, {x.T, x.H, x.d}, BF16, x.dev)) Py_RETURN_NONE;
+        Output out, lse;
         const int want = truth(a[12]);
-        if (want < 0) Py_RETURN_NONE;
-        if ((a[11] != Py_None || want) && !output(a[11], lse, {x.T, x.H}, FP32, x.dev)) Py_RETURN_NONE;
+        if (want < 0 || !out.ok(a[10], {x.T, x.H, x.d}, BF16, x.dev) || !lse.ok(a[11], {x.T, x.H}, FP32, x.dev, want))
+            Py_RETURN_NONE;
         const int nseq = (int)cu.size(0) - 1;
-        const size_t bytes = la_softmax_prefill_paged_workspace_size(nseq, x.T, x.H, x.Hkv, x.d, c.page, c.max_pages);
-        if (bytes) ws = make({(int64_t)bytes}, at::kByte, x.dev);
-        const la_status st = la_softmax_prefill_paged(
-            x.q.ptr(), x.k.ptr(), x.v.ptr(), (const int *)cu.ptr(), nseq, x.T, longest, x.H, x.Hkv, x.d, scale, c.k.ptr(),
-            c.v.ptr(), c.n_pages, c.page, (const int *)c.table.ptr(), c.max_pages, (const int *)c.lens.ptr(),
-            out.data_ptr(), lse.defined() ? (float *)lse.data_ptr() : nullptr, bytes ? ws.data_ptr() : nullptr, bytes,
-            stream_of(x.dev));
-        return result(st, out, lse);
+        const void *q = x.q.ptr(), *k = x.k.ptr(), *v = x.v.ptr();
+        const int *seqs = (const int *)cu.ptr();
+        const CachePtrs p(c);
+        const la_status st = [&] {
+            Unlocked free;
+            void *o = out.ptr(x.dev), *l = lse.ptr(x.dev);
+            Workspace ws(la_softmax_prefill_paged_workspace_size(nseq, x.T, x.H, x.Hkv, x.d, c.page, c.max_pages), x.dev);
+            return la_softmax_prefill_paged(q, k, v, seqs, nseq, x.T, longest, x.H, x.Hkv, x.d, scale, p.k, p.v,
+                                            c.n_pages, c.page, p.table, c.max_pages, p.lens, o, (float *)l, ws.at,
+                                            ws.bytes, stream_of(x.dev));
+        }();
+        return result(st, out.t, lse.t);
     });
 }
 
@@ -190,20 +235,22 @@ PyObject *decode_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
         Cache c;
         float scale;
         if (n != 12 || !x.ok(a) || !c.ok(a + 3, x, x.T) || !number(a[7], scale)) Py_RETURN_NONE;
-        at::Tensor out, lse, ws;
+        Output out, lse;
         const auto type = a[9] == Py_True ? FP32 : BF16;
-        if (!output(a[8], out, {x.T, x.H, x.d}, type, x.dev)) Py_RETURN_NONE;
         const int want = truth(a[11]);
-        if (want < 0) Py_RETURN_NONE;
-        if ((a[10] != Py_None || want) && !output(a[10], lse, {x.T, x.H}, FP32, x.dev)) Py_RETURN_NONE;
-        const size_t bytes = la_softmax_decode_paged_workspace_size(x.T, x.H, x.Hkv, x.d, c.page, c.max_pages);
-        if (bytes) ws = make({(int64_t)bytes}, at::kByte, x.dev);
-        const la_status st = la_softmax_decode_paged(
-            x.q.ptr(), x.k.ptr(), x.v.ptr(), x.T, x.H, x.Hkv, x.d, scale, c.k.ptr(), c.v.ptr(), c.n_pages, c.page,
-            (const int *)c.table.ptr(), c.max_pages, (const int *)c.lens.ptr(), out.data_ptr(),
-            type == FP32 ? LA_FP32 : LA_BF16, lse.defined() ? (float *)lse.data_ptr() : nullptr,
-            bytes ? ws.data_ptr() : nullptr, bytes, stream_of(x.dev));
-        return result(st, out, lse);
+        if (want < 0 || !out.ok(a[8], {x.T, x.H, x.d}, type, x.dev) || !lse.ok(a[10], {x.T, x.H}, FP32, x.dev, want))
+            Py_RETURN_NONE;
+        const void *q = x.q.ptr(), *k = x.k.ptr(), *v = x.v.ptr();
+        const CachePtrs p(c);
+        const la_status st = [&] {
+            Unlocked free;
+            void *o = out.ptr(x.dev), *l = lse.ptr(x.dev);
+            Workspace ws(la_softmax_decode_paged_workspace_size(x.T, x.H, x.Hkv, x.d, c.page, c.max_pages), x.dev);
+            return la_softmax_decode_paged(q, k, v, x.T, x.H, x.Hkv, x.d, scale, p.k, p.v, c.n_pages, c.page, p.table,
+                                           c.max_pages, p.lens, o, type == FP32 ? LA_FP32 : LA_BF16, (float *)l, ws.at,
+                                           ws.bytes, stream_of(x.dev));
+        }();
+        return result(st, out.t, lse.t);
     });
 }
 
@@ -219,19 +266,23 @@ PyObject *prefill_backward_varlen(PyObject *, PyObject *const *a, Py_ssize_t n) 
             !dout.sized({x.T, x.H, x.d}) || !cu.ok(a[6], INT32, 1, x.dev) || cu.size(0) < 1 || !small(cu.size(0)) ||
             !number(a[7], longest) || !number(a[8], scale))
             Py_RETURN_NONE;
-        at::Tensor dq, dk, dv;
-        if (!output(a[9], dq, {x.T, x.H, x.d}, BF16, x.dev) || !output(a[10], dk, {x.T, x.Hkv, x.d}, BF16, x.dev) ||
-            !output(a[11], dv, {x.T, x.Hkv, x.d}, BF16, x.dev))
+        Output dq, dk, dv;
+        if (!dq.ok(a[9], {x.T, x.H, x.d}, BF16, x.dev) || !dk.ok(a[10], {x.T, x.Hkv, x.d}, BF16, x.dev) ||
+            !dv.ok(a[11], {x.T, x.Hkv, x.d}, BF16, x.dev))
             Py_RETURN_NONE;
         const int nseq = (int)cu.size(0) - 1;
-        const size_t bytes = la_softmax_prefill_backward_varlen_workspace_size(nseq, x.T, x.H, x.Hkv, x.d);
-        at::Tensor ws = make({(int64_t)(bytes ? bytes : 256)}, at::kByte, x.dev);
-        const la_status st = la_softmax_prefill_backward_varlen(
-            x.q.ptr(), x.k.ptr(), x.v.ptr(), out.ptr(), (const float *)lse.ptr(), dout.ptr(), (const int *)cu.ptr(), nseq,
-            x.T, longest, x.H, x.Hkv, x.d, scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), bytes,
-            stream_of(x.dev));
+        const void *q = x.q.ptr(), *k = x.k.ptr(), *v = x.v.ptr(), *o = out.ptr(), *g = dout.ptr();
+        const float *l = (const float *)lse.ptr();
+        const int *seqs = (const int *)cu.ptr();
+        const la_status st = [&] {
+            Unlocked free;
+            void *to_q = dq.ptr(x.dev), *to_k = dk.ptr(x.dev), *to_v = dv.ptr(x.dev);
+            Workspace ws(la_softmax_prefill_backward_varlen_workspace_size(nseq, x.T, x.H, x.Hkv, x.d), x.dev);
+            return la_softmax_prefill_backward_varlen(q, k, v, o, l, g, seqs, nseq, x.T, longest, x.H, x.Hkv, x.d, scale,
+                                                      to_q, to_k, to_v, ws.at, ws.bytes, stream_of(x.dev));
+        }();
         if (st != LA_OK) return PyLong_FromLong(st);
-        return Py_BuildValue("(NNN)", THPVariable_Wrap(dq), THPVariable_Wrap(dk), THPVariable_Wrap(dv));
+        return Py_BuildValue("(NNN)", THPVariable_Wrap(dq.t), THPVariable_Wrap(dk.t), THPVariable_Wrap(dv.t));
     });
 }
 
@@ -247,9 +298,14 @@ PyObject *copy_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
         for (int i = 0; i < 4; ++i)
             if (!small(k.size(i))) Py_RETURN_NONE;
         if (!small(src.size(0))) Py_RETURN_NONE;
-        const la_status st =
-            la_cache_copy_pages(k.ptr(), v.ptr(), (int)k.size(0), (int)k.size(2), (int)k.size(1), (int)k.size(3),
-                                (const int *)src.ptr(), (const int *)dst.ptr(), (int)src.size(0), stream_of(dev));
+        const int pages = (int)k.size(0), heads = (int)k.size(1), page = (int)k.size(2), d = (int)k.size(3);
+        const int count = (int)src.size(0);
+        void *kp = k.ptr(), *vp = v.ptr();
+        const int *from = (const int *)src.ptr(), *to = (const int *)dst.ptr();
+        const la_status st = [&] {
+            Unlocked free;
+            return la_cache_copy_pages(kp, vp, pages, page, heads, d, from, to, count, stream_of(dev));
+        }();
         return st == LA_OK ? PyTuple_New(0) : PyLong_FromLong(st);
     });
 }

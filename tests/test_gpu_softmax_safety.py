@@ -1,6 +1,9 @@
 """Softmax attention calls where warps, kernels or threads meet: rows that do not
 fill a warp, kernels that start behind one that still runs, waits that run out,
 calls that block."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -80,3 +83,53 @@ def test_limits_do_not_count_the_kernel_in_front(kind):
     assert la.get_device_status() == la.LA_OK
     for x, y in zip(got, want):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("kind", ["prompt", "gradients", "chunk", "decode", "copy"])
+def test_other_threads_run_while_a_call_waits(kind):
+    """A call that blocks, here behind a full launch queue, does not hold up the
+    process's other Python threads."""
+    q, k, v, _, cu = packed([40], 4, 2, 7)
+    c = Cache([100], [40], 2, 16, 8)
+    g = torch.randn_like(q)
+    out, lse = la.softmax_prefill_varlen(q, k, v, cu, 40)
+    dq, dk, dv = (torch.empty_like(x) for x in (q, k, v))
+    one = [torch.empty_like(out[:1]), torch.empty_like(lse[:1])]
+    src, dst = (torch.tensor([i], dtype=torch.int32, device="cuda") for i in (0, 1))
+    call = {
+        "prompt": lambda: la.softmax_prefill_varlen(q, k, v, cu, 40, out=out, lse=lse),
+        "gradients": lambda: la.softmax_prefill_backward_varlen(q, k, v, out, lse, g, cu, 40, dq=dq, dk=dk, dv=dv),
+        "chunk": lambda: la.softmax_prefill_paged(q, k, v, cu, 40, c.k, c.v, c.table, c.lens, out=out, lse=lse),
+        "decode": lambda: la.softmax_decode_paged(q[:1], k[:1], v[:1], c.k, c.v, c.table, c.lens, out=one[0], lse=one[1]),
+        "copy": lambda: la.cache_copy_pages(c.k, c.v, src, dst),
+    }[kind]
+    call()
+    torch.cuda.synchronize()
+    ticks, stop = [], threading.Event()
+
+    def tick():
+        while not stop.is_set():
+            ticks.append(time.perf_counter())
+            time.sleep(0.002)
+    other = threading.Thread(target=tick)
+    other.start()
+    try:
+        torch.cuda._sleep(1_500_000_000)  # some 0.8 s: the launches behind it fill the queue
+        longest = began = 0.0
+        for _ in range(3000):
+            t0 = time.perf_counter()
+            call()
+            t1 = time.perf_counter()
+            if t1 - t0 > longest:
+                longest, began = t1 - t0, t0
+            if longest > 0.1:
+                break
+    finally:
+        stop.set()
+        other.join()
+    torch.cuda.synchronize()
+    assert la.get_device_status() == la.LA_OK
+    assert longest > 0.1, "no call blocked"
+    inside = [t for t in ticks if began < t < began + longest]
+    # a tick takes 2 ms and what the machine's scheduler adds: a fifth of them is plenty
+    assert len(inside) >= longest / 0.002 / 5, f"{len(inside)} ticks in {longest:.3f} s"
