@@ -488,6 +488,9 @@ LA_API la_status la_softmax_prefill_backward_varlen(const void *q, const void *k
  *   the new token, does the same and records LA_ERR_INVALID_ARGUMENT.
  *   The step reads the keys of all requests in equal shares per SM, so it
  *   needs no lengths on the host.  The result does not depend on timing.
+ *   The weights meet v as pairs of bf16, within 2^-16 of each.  An infinite
+ *   value in v whose weight is above zero gives infinity, with its sign, as in
+ *   prompts; a weight that underflows gives NaN there.
  * la_cache_copy_pages: page src[i] is copied to page dst[i] in both tensors,
  *   i < n (DEVICE int32).  Forks copy their ragged last page, compactions
  *   move pages to lower numbers.  A destination must not occur twice nor be

@@ -18,8 +18,8 @@
 // the row ends.  The group's heads are the rows or columns of m16n8k16 products:
 // with 8 or 16 of them, tcgen05 tiles of 128 rows would be 7/8 empty and need the
 // same bytes, while mma.sync from registers stays below the time the tile's bytes
-// take.  The weights meet V as a bf16 pair hi + lo (2^-17 of each), so
-// the output is as exact as its own type.
+// take.  The weights meet V as a bf16 pair hi + lo (within 2^-16 of each), so the
+// output is nearly as exact as its own type.
 //
 // 64 requests of 8192 keys, 64 heads over 8: 2.15 GB at 6.8 TB/s, 83 % of what DRAM
 // could nominally do, tensor pipe busy 16 %.  256 requests of up to 8192: 0.64 ms,
@@ -217,10 +217,18 @@ __device__ __forceinline__ float sd_sum(const float *red, int head, int d) {
     return x;
 }
 
-// bf16 pairs hi + lo of two fp32 values, each within 2^-17 or so
+// bf16 pairs hi + lo of two weights e >= 0, hi the next bf16 below e.  lo is then above
+// zero whenever e is, at most 2^-7 e, and rounded by at most 2^-16 e.  With the nearest
+// bf16 for hi, rounded by half of that, lo would be zero or negative for half of the
+// weights, and with an infinite value hi v + lo v would be NaN where the sum is infinite.
+__device__ __forceinline__ uint32_t sd_below(float e) {
+    const uint32_t bits = __float_as_uint(e);
+    return max(bits, 1u) - 1u;  // (0 stays 0)
+}
 __device__ __forceinline__ void sd_hi_lo(float a, float b, uint32_t &hi, uint32_t &lo) {
-    hi = pack_bf16x2(a, b);
-    lo = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+    const uint32_t x = sd_below(a), y = sd_below(b);
+    hi = __byte_perm(x, y, 0x7632);  // the upper halves
+    lo = pack_bf16x2(a - __uint_as_float(x & 0xffff0000u), b - __uint_as_float(y & 0xffff0000u));
 }
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {  // an 8 x 8 bf16 matrix over the warp, transposed
     uint32_t y;
