@@ -443,9 +443,11 @@ LA_API la_status la_softmax_prefill_varlen(const void *q, const void *k, const v
  * and the workspace (la_softmax_prefill_backward_varlen_workspace_size bytes,
  * 256-byte aligned) must not overlap the inputs or each other.  The gradient of
  * lse is not taken.  P and dS are rounded to bf16 once each for the products
- * that sum over them.  A value of dout that is not finite may reach dv of later
- * rows of the same sequence in the same 128 rows.  Otherwise as
- * la_softmax_prefill_varlen. */
+ * that sum over them.  Of values that are not finite, and beyond the rows that
+ * see them, one of dout may reach its feature of dv of later rows, one of q its
+ * feature of dk of later rows, and one of k its feature of dq of earlier rows,
+ * each in the same 128 rows of the sequence; a row of out that holds one, or a
+ * lse, has what its own dout has.  Otherwise as la_softmax_prefill_varlen. */
 LA_API size_t la_softmax_prefill_backward_varlen_workspace_size(int nseq, int total_tokens, int H,
                                                                 int Hkv, int d);
 

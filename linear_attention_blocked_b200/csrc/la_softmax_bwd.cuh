@@ -481,14 +481,20 @@ la_softmax_dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_cons
                         if (lane == 0) mbar_arrive(&cb->sum_full[wg]);
                         if (!wait(&cb->sum_full[wg], 1)) { ok = false; break; }
                     }
+                    // On the diagonal what is hidden stays 0, also where its dP - delta is not
+                    // finite.  (8 sequences of 60: 0.7 us; set to 0 once more, 1.3 us.)
+                    auto times_dp = [&](int lim) {
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const float4 de = rows[32 + q];
-                        pr[4 * q] *= __uint_as_float(x[4 * q]) - de.x;
-                        pr[4 * q + 1] *= __uint_as_float(x[4 * q + 1]) - de.y;
-                        pr[4 * q + 2] *= __uint_as_float(x[4 * q + 2]) - de.z;
-                        pr[4 * q + 3] *= __uint_as_float(x[4 * q + 3]) - de.w;
-                    }
+                        for (int q = 0; q < 16; ++q) {
+                            const float4 de = rows[32 + q];
+                            if (4 * q >= lim) pr[4 * q] *= __uint_as_float(x[4 * q]) - de.x;
+                            if (4 * q + 1 >= lim) pr[4 * q + 1] *= __uint_as_float(x[4 * q + 1]) - de.y;
+                            if (4 * q + 2 >= lim) pr[4 * q + 2] *= __uint_as_float(x[4 * q + 2]) - de.z;
+                            if (4 * q + 3 >= lim) pr[4 * q + 3] *= __uint_as_float(x[4 * q + 3]) - de.w;
+                        }
+                    };
+                    if (i == im[BI_BLK]) times_dp(r - wg * 64);
+                    else times_dp(0);
                     tmem_st_bf16x64(tdp, pr);  // likewise one rounding
                     tmem_wait_st();
                     tc_fence_before();

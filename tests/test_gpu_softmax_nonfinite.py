@@ -1,5 +1,5 @@
-"""Values that are not finite, in decode steps: what they reach and what they leave as
-it is."""
+"""Values that are not finite, in decode steps and in gradients: what they reach and
+what they leave as it is."""
 import pytest
 import torch
 
@@ -59,3 +59,60 @@ def test_a_token_alone_and_as_a_chunk_agree_on_infinities(heads):
     assert la.get_device_status() == la.LA_OK
     for x in (a, b):
         assert (x[..., ::3] == INF).all() and (x[..., 1::3] == -INF).all() and torch.isfinite(x[..., 2::3]).all()
+
+
+@pytest.mark.parametrize("bad", [INF, -INF, NAN])
+@pytest.mark.parametrize("at", [20, 200, 399])
+@pytest.mark.parametrize("heads", [(4, 2), (3, 3), (8, 1)], ids=str)
+def test_a_bad_output_gradient_stays_out_of_later_keys(heads, at, bad):
+    """dout of row `at` has no part in dk of later rows, nor in dq of other rows, nor in
+    dv of rows in later blocks of 128 or of other features: bit for bit what it is with
+    any other value there."""
+    q, k, v, _, cu = packed([400], *heads, seed=65)
+    g = torch.randn_like(q)
+    out, lse = la.softmax_prefill_varlen(q, k, v, cu, 400)
+    want = la.softmax_prefill_backward_varlen(q, k, v, out, lse, g, cu, 400)
+    g[at, 0, 3] = bad
+    dq, dk, dv = la.softmax_prefill_backward_varlen(q, k, v, out, lse, g, cu, 400)
+    assert la.get_device_status() == la.LA_OK
+    others = torch.arange(400, device="cuda") != at
+    assert torch.equal(dq[others], want[0][others]) and torch.equal(dq[at, 1:], want[0][at, 1:])
+    assert torch.equal(dk[at + 1:], want[1][at + 1:])
+    assert torch.equal(dk[:, 1:], want[1][:, 1:]) and torch.equal(dv[:, 1:], want[2][:, 1:])
+    block = (at // 128 + 1) * 128
+    assert torch.equal(dv[block:], want[2][block:])
+    features = torch.arange(128, device="cuda") != 3
+    assert torch.equal(dv[..., features], want[2][..., features])
+    # and what it reaches, it reaches
+    assert not torch.isfinite(dq[at, 0]).any() and not torch.isfinite(dk[:at + 1, 0]).any()
+    assert not torch.isfinite(dv[:at + 1, 0, 3]).any()
+
+
+@pytest.mark.parametrize("bad", [INF, NAN])
+@pytest.mark.parametrize("at", [20, 200, 399])
+@pytest.mark.parametrize("heads", [(4, 2), (3, 3), (8, 1)], ids=str)
+def test_a_bad_query_or_key_reaches_one_feature_of_its_block(heads, at, bad):
+    """q of row `at` may reach its feature of dk of later rows, k its feature of dq of
+    earlier ones, in the same 128 rows; nothing else of the rows that do not see it."""
+    q, k, v, _, cu = packed([400], *heads, seed=67)
+    g = torch.randn_like(q)
+
+    def grads(q, k):
+        out, lse = la.softmax_prefill_varlen(q, k, v, cu, 400)
+        return la.softmax_prefill_backward_varlen(q, k, v, out, lse, g, cu, 400)
+    want = grads(q, k)
+    features = torch.arange(128, device="cuda") != 3
+    q2, k2 = q.clone(), k.clone()
+    q2[at, 0, 3] = bad
+    dq, dk, dv = grads(q2, k)
+    others = torch.arange(400, device="cuda") != at
+    block = (at // 128 + 1) * 128
+    assert torch.equal(dq[others], want[0][others]) and torch.equal(dv[at + 1:], want[2][at + 1:])
+    assert torch.equal(dk[block:], want[1][block:])
+    assert torch.equal(dk[at + 1:][..., features], want[1][at + 1:][..., features])
+    k2[at, 0, 3] = bad
+    dq, _, _ = grads(q, k2)
+    assert torch.equal(dq[:at // 128 * 128], want[0][:at // 128 * 128])
+    assert torch.equal(dq[:at][..., features], want[0][:at][..., features])
+    assert torch.equal(dq[:, heads[0] // heads[1]:], want[0][:, heads[0] // heads[1]:])
+    assert la.get_device_status() == la.LA_OK
