@@ -136,10 +136,10 @@ bool number(PyObject *o, float &x) {
     x = (float)v;
     return true;
 }
-bool number(PyObject *o, int &x) {
+bool length(PyObject *o, int &x) {
     int overflow = 0;
     const long v = PyLong_Check(o) ? PyLong_AsLongAndOverflow(o, &overflow) : (overflow = 1, 0L);
-    if (overflow || v < INT32_MIN || v > INT32_MAX) return false;
+    if (overflow || v < 0 || v > INT32_MAX) return false;
     x = (int)v;
     return true;
 }
@@ -177,7 +177,7 @@ PyObject *prefill_varlen(PyObject *, PyObject *const *a, Py_ssize_t n) {
         float scale;
         int longest;
         if (n != 9 || !x.ok(a) || !cu.ok(a[3], INT32, 1, x.dev) || cu.size(0) < 1 || !small(cu.size(0)) ||
-            !number(a[4], longest) || !number(a[5], scale))
+            !length(a[4], longest) || !number(a[5], scale))
             Py_RETURN_NONE;
         Output out, lse;
         const int want = truth(a[8]);
@@ -206,7 +206,7 @@ PyObject *prefill_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
         float scale;
         int longest;
         if (n != 13 || !x.ok(a) || !cu.ok(a[3], INT32, 1, x.dev) || cu.size(0) < 1 || !small(cu.size(0)) ||
-            !number(a[4], longest) || !c.ok(a + 5, x, (int)cu.size(0) - 1) || !number(a[9], scale))
+            !length(a[4], longest) || !c.ok(a + 5, x, (int)cu.size(0) - 1) || !number(a[9], scale))
             Py_RETURN_NONE;
         Output out, lse;
         const int want = truth(a[12]);
@@ -264,7 +264,7 @@ PyObject *prefill_backward_varlen(PyObject *, PyObject *const *a, Py_ssize_t n) 
         if (n != 12 || !x.ok(a) || !out.ok(a[3], BF16, 3, x.dev) || !out.sized({x.T, x.H, x.d}) ||
             !lse.ok(a[4], FP32, 2, x.dev) || !lse.sized({x.T, x.H}) || !dout.ok(a[5], BF16, 3, x.dev) ||
             !dout.sized({x.T, x.H, x.d}) || !cu.ok(a[6], INT32, 1, x.dev) || cu.size(0) < 1 || !small(cu.size(0)) ||
-            !number(a[7], longest) || !number(a[8], scale))
+            !length(a[7], longest) || !number(a[8], scale))
             Py_RETURN_NONE;
         Output dq, dk, dv;
         if (!dq.ok(a[9], {x.T, x.H, x.d}, BF16, x.dev) || !dk.ok(a[10], {x.T, x.Hkv, x.d}, BF16, x.dev) ||

@@ -91,3 +91,20 @@ def test_calls_leave_nothing_behind():
         torch.cuda.synchronize()
         return torch.cuda.memory_allocated()
     assert calls(10) == calls(1000)
+
+
+def test_lengths_below_zero_raise_the_same(monkeypatch):
+    """max_seqlen = -1 and beyond 32 bits: a ValueError, however the call is marshalled."""
+    q, k, v, cu, cu_dev = packed([40], 4, 2, 5)
+    c = Cache([20], [40], 2, 16, 6)
+    out, lse = la.softmax_prefill_varlen(q, k, v, cu_dev, 40)
+    for _ in range(2):
+        for n in (-1, -(1 << 31), 1 << 31, -(1 << 40)):
+            with pytest.raises(ValueError):
+                la.softmax_prefill_varlen(q, k, v, cu_dev, n)
+            with pytest.raises(ValueError):
+                la.softmax_prefill_backward_varlen(q, k, v, out, lse, q.clone(), cu_dev, n)
+            with pytest.raises(ValueError):
+                la.softmax_prefill_paged(q, k, v, cu_dev, n, c.k, c.v, c.table, c.lens)
+        monkeypatch.setattr(softmax, "_marshal", None)
+    assert la.get_device_status() == la.LA_OK
