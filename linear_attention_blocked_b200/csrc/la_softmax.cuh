@@ -66,6 +66,7 @@ constexpr int SMX_SMEM = SMX_STAT + 2 * BLK * 8;            // (1024-byte aligne
 static_assert(SMX_SMEM <= 227 * 1024, "shared memory of one CTA");
 constexpr uint32_t SMX_TM_S = 0, SMX_TM_O = 256;            // tile t: + 128 t
 constexpr int HDR_TICKET2 = 3;                              // second ticket counter of the workspace header
+constexpr int HDR_READY = 4;                                // gradients: dkv has seen the tables and rows
 constexpr int SMX_SLOTS = 4;                                // item queue
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr int SMX_CTAS = 148;                               // split: runs of key tiles
@@ -1050,6 +1051,7 @@ __device__ __forceinline__ void softmax_schedule(const SoftmaxScheduleParams &s)
     if (tid == 0) {
         s.hdr[HDR_TICKET] = 0;
         s.hdr[HDR_TICKET2] = 0;
+        s.hdr[HDR_READY] = 0;
         carry_sh = 0;
         if (bad) {
             s.hdr[HDR_TOTAL] = 0;

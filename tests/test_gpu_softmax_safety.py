@@ -133,3 +133,30 @@ def test_other_threads_run_while_a_call_waits(kind):
     inside = [t for t in ticks if began < t < began + longest]
     # a tick takes 2 ms and what the machine's scheduler adds: a fifth of them is plenty
     assert len(inside) >= longest / 0.002 / 5, f"{len(inside)} ticks in {longest:.3f} s"
+
+
+@pytest.mark.parametrize("heads,lens", [((4, 4), [200]), ((8, 1), [40, 90]), ((16, 2), [700, 33]), ((64, 8), [1])], ids=str)
+def test_gradients_in_one_workspace_follow_their_inputs(heads, lens):
+    """Calls one behind the other in one workspace, with fewer key blocks than SMs, so
+    that dq starts on SMs that dk and dv never used: every call's gradients are those of
+    its own inputs, lse and tables."""
+    sets, total = [], sum(lens)
+    for seed in range(3):
+        order = lens[seed % len(lens):] + lens[:seed % len(lens)]
+        q, k, v, _, cu = packed(order, *heads, seed)
+        g = torch.randn_like(q)
+        out, lse = la.softmax_prefill_varlen(q, k, v, cu, max(lens))
+        want = la.softmax_prefill_backward_varlen(q, k, v, out, lse, g, cu, max(lens))
+        sets.append(((q, k, v, out, lse, g, cu, max(lens)), want))
+    torch.cuda.synchronize()
+    size = la.lib().la_softmax_prefill_backward_varlen_workspace_size(len(lens), total, *heads, 128)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    got = [[torch.empty_like(x) for x in sets[0][1]] for _ in range(60)]
+    for _ in range(5):
+        for i, (dq, dk, dv) in enumerate(got):
+            la.softmax_prefill_backward_varlen(*sets[i * i % 3][0], dq=dq, dk=dk, dv=dv, workspace=ws)
+        torch.cuda.synchronize()
+        for i, xs in enumerate(got):
+            for x, y in zip(xs, sets[i * i % 3][1]):
+                assert torch.equal(x, y), i
+    assert la.get_device_status() == la.LA_OK
