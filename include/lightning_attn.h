@@ -546,7 +546,8 @@ LA_API const char *la_status_string(la_status status);
  * la_set_wait_limit_ns: upper bound for every device-side wait (mbarrier
  *   phases, the cross-SM segment hand-off).  Default 2e9 ns.  A wait that runs
  *   out records LA_ERR_TIMEOUT and the kernel finishes without hanging.
- *   0 restores the default.
+ *   0 restores the default.  (What a softmax kernel has in flight when it ends,
+ *   it waits for up to the default whatever the limit.)
  * la_set_segment_len: tokens per segment of the cross-SM scan; 0 = automatic,
  *   otherwise a positive multiple of 128.  Changes only speed and rounding.
  * la_debug_inject: fault injection made on the host side, for tests.

@@ -215,6 +215,15 @@ __device__ __forceinline__ bool ctrl_warp_wait(uint64_t *bar, uint32_t parity, u
     return __all_sync(0xffffffffu, ctrl_wait(bar, parity, limit_ns, status, cb)) != 0;
 }
 
+// Before a CTA ends, what it has in flight does: copies into its shared memory, products
+// into its TMEM.  They end by themselves, also where a wait has run out, and take
+// microseconds; so this wait has a limit of its own, which no setting shortens.
+constexpr unsigned long long DRAIN_NS = 2000000000ull;
+__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
+    int go_on = 0;
+    la_wait(bar, parity, globaltimer_ns() + DRAIN_NS, &go_on);
+}
+
 // The next item of the queue; a role reads the fields of its MASK.
 template <uint32_t MASK>
 __device__ __forceinline__ bool smx_next(uint32_t &it, int (&item)[SI_FIELDS], int lane,
@@ -620,8 +629,7 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
             // every issued copy must land before the CTA exits
             const uint32_t first = n > SMX_STAGES ? n - SMX_STAGES : 0;
             for (uint32_t i = first; i < n; ++i) {
-                int dummy = 0;
-                la_wait(&cb->kv_full[i % SMX_STAGES], (i / SMX_STAGES) & 1, globaltimer_ns() + p.wait_limit_ns, &dummy);
+                drain_wait(&cb->kv_full[i % SMX_STAGES], (i / SMX_STAGES) & 1);
             }
             if (!ok) cb->abort = 1;
         } else if (warp == 1) {
@@ -726,8 +734,7 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
                     if ((MASK >> f) & 1) cur[f] = nxt[f];
             }
             tc_commit_w(&cb->fin);
-            int dummy = 0;
-            la_wait(&cb->fin, 0, globaltimer_ns() + p.wait_limit_ns, &dummy);
+            drain_wait(&cb->fin, 0);
         } else if (warp == 2) {
             // ===================== Q tiles =====================
             const uint64_t pol = policy_evict_first();
@@ -750,8 +757,7 @@ la_softmax_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_
             }
             for (int t = 0; t < 2; ++t)
                 if (n[t] > 0) {
-                    int dummy = 0;
-                    la_wait(&cb->q_full[t], (n[t] - 1) & 1, globaltimer_ns() + p.wait_limit_ns, &dummy);
+                    drain_wait(&cb->q_full[t], (n[t] - 1) & 1);
                 }
         } else if (p.new_k) {
             // ===================== new tokens into their pages =====================

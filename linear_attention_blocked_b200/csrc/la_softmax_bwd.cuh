@@ -275,8 +275,7 @@ la_softmax_dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_cons
                     }
             }
             for (uint32_t i = n > 2 ? n - 2 : 0; i < n; ++i) {  // copies land before the CTA exits
-                int dummy = 0;
-                la_wait(&cb->q_full[i & 1], (i >> 1) & 1, globaltimer_ns() + p.wait_limit_ns, &dummy);
+                drain_wait(&cb->q_full[i & 1], (i >> 1) & 1);
             }
             if (!ok) cb->abort = 1;
         } else if (warp == 1) {
@@ -348,8 +347,7 @@ la_softmax_dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_cons
                 for (int f = 0; f < BI_FIELDS; ++f) cur[f] = nxt[f];
             }
             tc_commit_w(&cb->fin);
-            int dummy = 0;
-            la_wait(&cb->fin, 0, globaltimer_ns() + p.wait_limit_ns, &dummy);
+            drain_wait(&cb->fin, 0);
         } else if (warp == 2) {
             // ===================== K and V tiles =====================
             const uint64_t pol = policy_evict_first();
@@ -366,8 +364,7 @@ la_softmax_dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_cons
                 ++n;
             }
             if (n > 0) {
-                int dummy = 0;
-                la_wait(&cb->kv_full, (n - 1) & 1, globaltimer_ns() + p.wait_limit_ns, &dummy);
+                drain_wait(&cb->kv_full, (n - 1) & 1);
             }
         } else {
             // ===================== rows of the steps =====================
@@ -708,8 +705,7 @@ la_softmax_dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                     }
             }
             for (uint32_t i = n > DQ_STAGES ? n - DQ_STAGES : 0; i < n; ++i) {
-                int dummy = 0;
-                la_wait(&cb->kv_full[i % DQ_STAGES], (i / DQ_STAGES) & 1, globaltimer_ns() + p.wait_limit_ns, &dummy);
+                drain_wait(&cb->kv_full[i % DQ_STAGES], (i / DQ_STAGES) & 1);
             }
             if (!ok) cb->abort = 1;
         } else if (warp == 1) {
@@ -778,8 +774,7 @@ la_softmax_dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                 for (int f = 0; f < BI_FIELDS; ++f) cur[f] = nxt[f];
             }
             tc_commit_w(&cb->fin);
-            int dummy = 0;
-            la_wait(&cb->fin, 0, globaltimer_ns() + p.wait_limit_ns, &dummy);
+            drain_wait(&cb->fin, 0);
         } else if (warp == 2) {
             // ===================== Q and g tiles =====================
             const uint64_t pol = policy_evict_first();
@@ -796,8 +791,7 @@ la_softmax_dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_const
                 ++n;
             }
             if (n > 0) {
-                int dummy = 0;
-                la_wait(&cb->q_full, (n - 1) & 1, globaltimer_ns() + p.wait_limit_ns, &dummy);
+                drain_wait(&cb->q_full, (n - 1) & 1);
             }
         }
     } else {

@@ -187,8 +187,7 @@ static_assert(sizeof(SoftmaxDecodeShared<DecodeShape<16, 3>>) <= 900 &&
 template <class S>
 __device__ __forceinline__ void sd_drain(uint32_t it, SoftmaxDecodeCtrl *cb, const SoftmaxDecodeParams &p) {
     for (uint32_t i = it > S::STAGES ? it - S::STAGES : 0; i < it; ++i) {  // copies land before the CTA exits
-        int dummy = 0;
-        la_wait(&cb->full[i % S::STAGES], (i / S::STAGES) & 1, globaltimer_ns() + p.wait_limit_ns, &dummy);
+        drain_wait(&cb->full[i % S::STAGES], (i / S::STAGES) & 1);
     }
 }
 

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import linear_attention_blocked_b200 as la
-from softmax_util import Cache, gradients64, packed
+from softmax_util import Cache, attention64, check, gradients64, packed
 
 pytestmark = pytest.mark.gpu
 S = 128 ** -0.5
@@ -34,10 +34,10 @@ def test_odd_numbers_of_rows(lens, heads):
             assert over <= 1, f"d{name} of tokens {a}-{b} off by {over:.2f} of its bound"
 
 
-def long_call():
+def long_call(past=400000):
     """A call of some 5 ms on 100 of the SMs: one new token of 200 heads behind 400000
     cached ones that they share.  The SMs left over take the next kernel's CTAs at once."""
-    past, page = 400000, 128
+    page = 128
     pages = past // page + 1
     gen = torch.Generator(device="cuda").manual_seed(3)
     kc, vc = (torch.randn(pages, 1, page, 128, generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(2))
@@ -160,3 +160,39 @@ def test_gradients_in_one_workspace_follow_their_inputs(heads, lens):
             for x, y in zip(xs, sets[i * i % 3][1]):
                 assert torch.equal(x, y), i
     assert la.get_device_status() == la.LA_OK
+
+
+@pytest.mark.parametrize("kind", ["prompt", "gradients"])
+def test_waits_that_run_out(kind):
+    """A limit far below the time of an item, for whose end warps wait: the kernels give
+    up, say so, and leave everything behind them as it should be."""
+    lens, heads = [300, 1, 129], (6, 2)
+    q, k, v, cu, cu_dev = packed(lens, *heads, seed=71)
+    g = torch.randn_like(q)
+    if kind == "prompt":
+        long = long_call(800000)
+    else:
+        x = [torch.randn(400000, 1, 128, device="cuda", dtype=torch.bfloat16) for _ in range(5)]
+        lse = torch.zeros(400000, 1, device="cuda")
+        cu_long = torch.tensor([0, 400000], dtype=torch.int32, device="cuda")
+
+        def long():
+            return la.softmax_prefill_backward_varlen(*x[:4], lse, x[4], cu_long, 400000)
+    try:
+        la.set_wait_limit_ns(100_000)
+        long()
+        torch.cuda.synchronize()
+    finally:
+        la.set_wait_limit_ns(0)
+    assert la.get_device_status() == la.LA_ERR_TIMEOUT
+    out, lse = la.softmax_prefill_varlen(q, k, v, cu_dev, max(lens))
+    got = la.softmax_prefill_backward_varlen(q, k, v, out, lse, g, cu_dev, max(lens))
+    assert la.get_device_status() == la.LA_OK
+    for a, b in zip(cu[:-1], cu[1:]):
+        check(out[a:b], lse[a:b], attention64(q[a:b], k[a:b], v[a:b], 0, S), b - a)
+        for y, (want, bound) in zip(got, gradients64(q[a:b], k[a:b], v[a:b], g[a:b], S).values()):
+            assert ((y[a:b].double() - want).abs() <= bound).all()
+    if kind == "prompt":
+        first, again = long(), long()
+        assert la.get_device_status() == la.LA_OK
+        assert all(torch.isfinite(y).all() and torch.equal(y, z) for y, z in zip(first, again))
