@@ -196,3 +196,38 @@ def test_waits_that_run_out(kind):
         first, again = long(), long()
         assert la.get_device_status() == la.LA_OK
         assert all(torch.isfinite(y).all() and torch.equal(y, z) for y, z in zip(first, again))
+
+
+def test_calls_from_several_threads():
+    """Threads with a stream each call at once, as the released interpreter lock allows:
+    the same results as one thread's."""
+    def work(seed):
+        lens = [40, 300, 7 + seed]
+        q, k, v, _, cu = packed(lens, 16, 2, seed)
+        c = Cache([500, 30, 900], [300, 300, 300], 2, 32, seed)
+        g = torch.randn(q.shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda",
+                        dtype=torch.bfloat16)
+        got = []
+        for _ in range(30):
+            out, lse = la.softmax_prefill_varlen(q, k, v, cu, 300)
+            got = [out, lse, *la.softmax_prefill_backward_varlen(q, k, v, out, lse, g, cu, 300),
+                   *la.softmax_prefill_paged(q, k, v, cu, 300, c.k, c.v, c.table, c.lens),
+                   *la.softmax_decode_paged(q[:3], k[:3], v[:3], c.k, c.v, c.table, c.lens)]
+        torch.cuda.current_stream().synchronize()
+        return got
+    want = [work(seed) for seed in range(4)]
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def threaded(seed):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got[seed] = work(seed)
+    threads = [threading.Thread(target=threaded, args=(seed,)) for seed in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert la.get_device_status() == la.LA_OK
+    for x, y in zip(got, want):
+        assert x is not None and all(torch.equal(a, b) for a, b in zip(x, y))
