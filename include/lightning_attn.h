@@ -411,7 +411,7 @@ LA_API la_status la_prefill_backward_varlen(const void *q, const void *k, const 
  *   out          device bf16 [total_tokens, H, d].
  *   lse          device fp32 [total_tokens, H], or NULL.  The backward pass
  *                needs it; with it partial results over disjoint keys can be
- *                joined.
+ *                joined (results, not gradients: see the backward pass).
  *   workspace    la_softmax_prefill_varlen_workspace_size bytes, 256-byte
  *                aligned, as for la_prefill; NULL will do where that is 0.
  * Scores, maxima, sums and outputs are accumulated in fp32; the weights are
@@ -438,7 +438,9 @@ LA_API la_status la_softmax_prefill_varlen(const void *q, const void *k, const v
  * dk and dv are summed over the query heads of their group, in fp32 and in a
  * fixed order (no atomics).  out and lse are those of the forward call.  The
  * first 128 rows of a sequence take delta as sum_s P_ts dout_t . v_s, which the
- * rounding of out to bf16 does not touch.  dout,
+ * rounding of out to bf16 does not touch.  With an out and a lse that were joined
+ * with results over other keys the gradients of those rows are therefore wrong,
+ * and nothing reports it.  dout,
  * dq: bf16 [total_tokens, H, d]; dk, dv: bf16 [total_tokens, Hkv, d]; the four
  * and the workspace (la_softmax_prefill_backward_varlen_workspace_size bytes,
  * 256-byte aligned) must not overlap the inputs or each other.  The gradient of

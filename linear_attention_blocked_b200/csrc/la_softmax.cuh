@@ -42,7 +42,7 @@
 // What bounds it: the exponentials (16 a cycle and SM) take as many cycles as the two
 // products, and an S product reads both operands from shared memory, at little more
 // than half its rate.  8192 tokens, 16 heads over 2: 215 us, 1278 TFLOP/s of causal
-// pairs, both units busy 62 % of the cycles.  32768 tokens, 32 heads over 4: 7.0 to
+// pairs, both units busy 63 % of the cycles.  32768 tokens, 32 heads over 4: 7.0 to
 // 7.5 ms, 1170 to 1250 TFLOP/s, at the power limit (clock near 1.6 of 1.965 GHz).
 // Slower or no faster there: a polynomial for part of the exponentials, four softmax
 // warpgroups of half a row, two MMA warps, P handed over in halves.

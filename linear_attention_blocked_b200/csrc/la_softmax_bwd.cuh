@@ -26,8 +26,8 @@
 // dq is off by 0.0023 of its norm instead of 0.0037 (dS and the result, rounded to
 // bf16, alone make 0.0023).  8 sequences of 60, 64 heads over 8: 3.7 us more.
 //
-// 8192 tokens, 16 heads over 2: dk and dv 424 us, 1297 TFLOP/s, tensor pipe busy
-// 64 %; dq 277 us, 1488 TFLOP/s, 74 %.  What is left is the way from a product
+// 8192 tokens, 16 heads over 2: dk and dv 447 us at 1.62 GHz, 1229 TFLOP/s, tensor pipe
+// busy 66 %; dq 299 us at 1.58 GHz, 1377 TFLOP/s, 75 %.  What is left is the way from a product
 // through TMEM, the exponentials or the sums and back to the next product.
 #pragma once
 #include "la_softmax.cuh"

@@ -22,8 +22,9 @@
 // output is nearly as exact as its own type.
 //
 // 64 requests of 8192 keys, 64 heads over 8: 2.15 GB at 6.8 TB/s, 83 % of what DRAM
-// could nominally do, tensor pipe busy 16 %.  256 requests of up to 8192: 0.64 ms,
-// 6.7 TB/s; one request of 524288 keys 0.325 ms, 6.6 TB/s.
+// could nominally do, tensor pipe busy 16 %.  256 requests of up to 8192: 0.645 ms,
+// 6.7 TB/s; one request of 524288 keys 0.327 ms, 6.6 TB/s: 90 % of what a kernel that
+// only reads gets.
 #pragma once
 #include "la_softmax.cuh"
 

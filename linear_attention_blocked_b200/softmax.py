@@ -275,8 +275,9 @@ def softmax_prefill_varlen(q, k, v, cu_seqlens, max_seqlen: int, scale=None, out
 def softmax_prefill_backward_varlen(q, k, v, out, lse, dout, cu_seqlens, max_seqlen: int, scale=None, dq=None, dk=None,
                                     dv=None, workspace=None, stream=None):
     """la_softmax_prefill_backward_varlen: gradients of softmax_prefill_varlen
-    for dL/dout; out and lse are what that call returned, scale what it was
-    given.  Returns (dq [T, H, d], dk, dv [T, Hkv, d]) in bf16."""
+    for dL/dout; out and lse are what that call returned (not joined with results
+    over other keys), scale what it was given.  Returns (dq [T, H, d], dk, dv
+    [T, Hkv, d]) in bf16."""
     if stream is None and workspace is None and _module() is not None:
         done = _short(_marshal.prefill_backward_varlen(q, k, v, out, lse, dout, cu_seqlens, max_seqlen,
                                                        SCALE if scale is None else scale, dq, dk, dv),
